@@ -454,6 +454,95 @@ int qlinear_rotate_next(const uint8_t* a_codes, const float* s, int bits_a, cons
 int quantize_rotated(const void* Xrot, int dtype, int T, int d, int bits, void* codes_out, float* norms_out,
                      void* stream);
 
+/* ---- block-scaled FP8 layers -------------------------------------------------
+ * The 8-bit linear layer with a scale for each block of 128 values, and what
+ * adapting such a layer needs: its weight and input gradients from 8-bit
+ * codes.  (The pages have no counterpart: like qlinear_fp8_levels this is a
+ * deployment variant for 8-bit tensor cores.  On rotated operands, x' = Pi x
+ * and W' = W Pi^T, it computes the same layer, as the rotation cancels.)
+ *
+ * Codes are OCP E4M3FN bytes; a scale is one E8M0 byte b, s = 2^(b - 127); the
+ * value held is code * s.  An activation row has a scale for each 128
+ * consecutive values, a weight matrix one for each 128 x 128 block; blocks at
+ * the right and lower edge may be short.  The quantisers choose
+ *   s = the smallest power of two with amax / s <= 448, at least 2^-117,
+ * amax the largest finite |value| of the block, and round value / s to
+ * nearest even.  NaN and infinities become NaN codes (0x7F / 0xFF) and do not
+ * count for amax.  Every decoded value is exact in BF16.
+ */
+
+/*
+ * quantize_fp8 -- codes and scales of the rows of act(X).
+ *   X          device [T, d], RBQ_BF16 or RBQ_F32, 16-byte aligned
+ *   T, d       rows (0 is a valid no-op); width, a multiple of 16
+ *   activation RBQ_ACT_NONE or RBQ_ACT_GELU (fp32; the normal CDF by
+ *              Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7)
+ *   codes      device uint8 [T, d], 16-byte aligned
+ *   scales     device uint8 [T, ceil(d / 128)]
+ *   x_codes, x_scales  with RBQ_ACT_GELU: the same of X itself, an 8-bit
+ *              checkpoint for gelu_backward_fp8; both NULL for none
+ * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
+ */
+int quantize_fp8(const void* X, int dtype, int T, int d, int activation, uint8_t* codes, uint8_t* scales,
+                 uint8_t* x_codes, uint8_t* x_scales, void* stream);
+
+/*
+ * quantize_weights_fp8 -- codes and scales of a weight matrix.
+ *   W        device [N, K], RBQ_BF16 or RBQ_F32, 16-byte aligned
+ *   K        a multiple of 16
+ *   codes    device uint8 [N, K], 16-byte aligned
+ *   scales   device uint8 [ceil(N / 128), ceil(K / 128)]
+ *   codes_t, scales_t  the same of W^T ([K, N] and [ceil(K / 128),
+ *            ceil(N / 128)]; N a multiple of 16), the weights of the input
+ *            gradient; both NULL for none
+ * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
+ */
+int quantize_weights_fp8(const void* W, int dtype, int N, int K, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                         uint8_t* scales_t, void* stream);
+
+/*
+ * qlinear_fp8 -- the layer on these codes:
+ *   Y[m, n] = bf16( sum_k (sa[m, k/128] qa[m, k]) (sw[n/128, k/128] qw[n, k]) ),
+ * fp32 accumulation on the tensor cores (tcgen05 kind::mxf8f6f4).  The input
+ * gradient of a layer is the same call on the codes of dY and of W^T.
+ *   a_codes, a_scales  device, [M, K] and [M, ceil(K / 128)]
+ *   w_codes, w_scales  device, [N, K] and [ceil(N / 128), ceil(K / 128)]
+ *   M, N     at most 2^30; K a multiple of 16
+ *   Y        device uint16 BF16 [M, N]
+ * Alignment: codes 16-byte.  No workspace.
+ * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
+ */
+int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                int M, int N, int K, uint16_t* Y, void* stream);
+
+/*
+ * qlinear_fp8_wgrad -- the layer's weight gradient from the codes kept of its
+ * input:  dW[n, k] = sum_m dY[m, n] (sa[m, k/128] qa[m, k]),
+ * on BF16 operands (the decoded codes are exact in BF16), fp32 accumulation.
+ *   dY                 device uint16 BF16 [M, N], 16-byte aligned; N a multiple of 8
+ *   a_codes, a_scales  device, [M, K] and [M, ceil(K / 128)]; K a multiple of 16
+ *   dW                 device [N, K], `dtype` RBQ_BF16 or RBQ_F32, 16-byte
+ *                      aligned; overwritten (zeros when M is 0)
+ * Workspace from a stream-ordered memory pool: M*K*2 bytes, and 4*N*K for each
+ * part when the tokens are split.
+ * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
+ */
+int qlinear_fp8_wgrad(const uint16_t* dY, const uint8_t* a_codes, const uint8_t* a_scales, int M, int N, int K,
+                      void* dW, int dtype, void* stream);
+
+/*
+ * gelu_backward_fp8 -- the GELU's backward pass from the 8-bit checkpoint of
+ * its input:  dX = bf16( dH (Phi(x) + x phi(x)) ),  x = code * s.
+ *   dH                 device uint16 BF16 [T, d], 16-byte aligned; d a multiple of 16
+ *   x_codes, x_scales  device, from quantize_fp8 (x_codes 16-byte aligned)
+ *   dX                 device uint16 BF16 [T, d], 16-byte aligned; may be dH itself
+ *   codes, scales      the codes and scales of dX (as quantize_fp8 gives
+ *                      them), for the product that follows; both NULL for none
+ * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
+ */
+int gelu_backward_fp8(const uint16_t* dH, const uint8_t* x_codes, const uint8_t* x_scales, int T, int d, uint16_t* dX,
+                      uint8_t* codes, uint8_t* scales, void* stream);
+
 /* ---- quantised layer files ------------------------------------------------
  * The pages' "quantized model file" (INT8-convrot, section 1): the quantised
  * weights, their quantisation parameters (scale, zero point or row norms) and

@@ -62,6 +62,9 @@ fused.qlinear_         the same on the code layer: a pure-Python triple
 quant.quantize_        steps 2-4 alone: quantize_rotated(Pi x) reproduces
   rotated              quantize_act(x, Pi) exactly; brute-force nearest
                        level on a tiny case
+fp8.fp8_encode         PyTorch's float8_e4m3fn conversion; scale bounds
+                       448 s >= amax > 224 s; hand-made blocks
+fp8.gelu_slope         central differences of x Phi(x)
 =====================  ===================================================
 """
 
@@ -75,6 +78,7 @@ from .quant import (assign_codes, pack_codes, unpack_codes, quantize_act, quanti
 from .qlinear import (qlinear, qlinear_int8, qlinear_int8_asym, int8_levels, qlinear_int8_levels,
                       e4m3_round, fp8_levels, qlinear_fp8_levels)
 from .fused import gelu, qlinear_int8_rotate_next, qlinear_rotate_next
+from .fp8 import fp8_scale_exponent, fp8_encode, fp8_scales, fp8_decode, gelu_slope
 
 __all__ = [
     "splitmix64", "rpbh_draw", "hadamard", "rpbh_matrix", "rpbh_rows", "rpbh_apply",
@@ -84,4 +88,5 @@ __all__ = [
     "quantize_weights_int8_asym", "rotate_only", "EPS", "qlinear", "qlinear_int8",
     "qlinear_int8_asym", "int8_levels", "qlinear_int8_levels", "e4m3_round", "fp8_levels",
     "qlinear_fp8_levels", "gelu", "qlinear_int8_rotate_next", "qlinear_rotate_next",
+    "fp8_scale_exponent", "fp8_encode", "fp8_scales", "fp8_decode", "gelu_slope",
 ]

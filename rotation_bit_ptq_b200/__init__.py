@@ -70,6 +70,11 @@ SIGNATURES = {
     "qlinear_int8_rotate_next": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, _P]),
     "qlinear_rotate_next": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
     "quantize_rotated": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "quantize_fp8": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "quantize_weights_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "qlinear_fp8": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "qlinear_fp8_wgrad": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P]),
+    "gelu_backward_fp8": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -694,3 +699,7 @@ def selftest_wait_limit(out, stream=None):
     if not (out.is_cuda and out.dtype == torch.int32 and out.numel() >= 1):
         raise ValueError("out must be a CUDA int32 tensor with at least one element")
     _check(lib().rbq_selftest_wait_limit(_P(out.data_ptr()), _stream(stream)), "rbq_selftest_wait_limit")
+
+
+from ._fp8 import (fp8_blocks, gelu_backward_fp8, linear_fp8, qlinear_fp8, qlinear_fp8_wgrad,  # noqa: E402,F401
+                   quantize_fp8, quantize_weights_fp8)

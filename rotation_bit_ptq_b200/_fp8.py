@@ -1,0 +1,265 @@
+"""The block-scaled FP8 layer: binding of quantize_fp8, quantize_weights_fp8,
+qlinear_fp8, qlinear_fp8_wgrad and gelu_backward_fp8 (include/rbq.h), and
+linear_fp8, the layer as a differentiable function.
+
+Codes are torch.float8_e4m3fn and scales torch.float8_e8m0fnu tensors, so
+``codes.float()`` times ``scale.float()`` of its block is the value held.
+"""
+
+import contextlib
+
+from . import (RBQ_ACT_GELU, RBQ_ACT_NONE, _ACTS, _check, _dtype_code, _need_cuda, _need_shape, check_same_device, lib)
+
+BLOCK = 128
+
+
+def fp8_blocks(n):
+    """Scale blocks along n values."""
+    return -(-int(n) // BLOCK)
+
+
+def check_fp8_width(n, name, step=16):
+    """Widths of FP8 rows: whole 16-byte pieces (pure Python, no device)."""
+    if n <= 0 or n % step:
+        raise ValueError(f"{name} must be a positive multiple of {step}, got {n}")
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The operands' device current and, when a stream is given, the current
+    stream too, so that what the call allocates belongs to the stream it is
+    written on."""
+    import torch
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            yield
+
+
+def _call(name, device, stream, *args):
+    """lib().name(*args, stream) with `device` current; tensors go as pointers."""
+    import torch
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    fn = getattr(lib(), name)
+    if stream is None and torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with _on(device, stream):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(device, stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _matrix(t, name, dtype=None):
+    _need_cuda(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+
+
+def _codes(codes, scale, rows_per_scale, name):
+    """Checks a matrix of codes and its scales; returns its shape."""
+    import torch
+    _matrix(codes, f"{name}_codes", torch.float8_e4m3fn)
+    _matrix(scale, f"{name}_scale", torch.float8_e8m0fnu)
+    n, d = codes.shape
+    check_fp8_width(d, f"the width of {name}_codes")
+    _need_shape(scale, (n if rows_per_scale == 1 else fp8_blocks(n), fp8_blocks(d)), f"{name}_scale")
+    return n, d
+
+
+def _out(t, shape, dtype, device, stream, name):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
+    _need_cuda(t, name, dtype)
+    _need_shape(t, shape, name)
+    return t
+
+
+def quantize_fp8(X, activation=None, checkpoint=False, codes=None, scale=None, stream=None):
+    """E4M3 codes [T, d] and E8M0 scales [T, ceil(d / 128)] of the rows of X
+    (bfloat16 or float32), or of GELU(X) with activation='gelu'.
+
+    checkpoint=True (with 'gelu') also returns the codes and scales of X
+    itself, from which gelu_backward_fp8 takes the gradient: (codes, scale,
+    x_codes, x_scale).  d a multiple of 16."""
+    import torch
+    _matrix(X, "X")
+    dtype = _dtype_code(X)
+    if activation not in _ACTS:
+        raise ValueError("activation must be None, 'none' or 'gelu'")
+    act = _ACTS[activation]
+    if checkpoint and act == RBQ_ACT_NONE:
+        raise ValueError("checkpoint goes with an activation: without one the codes are X's own")
+    T, d = X.shape
+    check_fp8_width(d, "the width of X")
+    dev = X.device
+    codes = _out(codes, (T, d), torch.float8_e4m3fn, dev, stream, "codes")
+    scale = _out(scale, (T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream, "scale")
+    check_same_device(X, codes, scale)
+    if not checkpoint:
+        _call("quantize_fp8", dev, stream, X, dtype, T, d, act, codes, scale, None, None)
+        return codes, scale
+    x_codes = _empty((T, d), torch.float8_e4m3fn, dev, stream)
+    x_scale = _empty((T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream)
+    _call("quantize_fp8", dev, stream, X, dtype, T, d, act, codes, scale, x_codes, x_scale)
+    return codes, scale, x_codes, x_scale
+
+
+def quantize_weights_fp8(W, transposed=False, codes=None, scale=None, stream=None):
+    """E4M3 codes [N, K] and E8M0 scales [ceil(N / 128), ceil(K / 128)] of a
+    weight matrix (bfloat16 or float32), one scale per 128 x 128 block.
+
+    transposed=True also returns the codes and scales of W^T, the weights of
+    the layer's input gradient: (codes, scale, codes_t [K, N], scale_t).
+    K a multiple of 16, and N too when transposed."""
+    import torch
+    _matrix(W, "W")
+    dtype = _dtype_code(W)
+    N, K = W.shape
+    check_fp8_width(K, "the width of W")
+    if transposed and N:
+        check_fp8_width(N, "the height of W (the width of its transpose)")
+    dev = W.device
+    codes = _out(codes, (N, K), torch.float8_e4m3fn, dev, stream, "codes")
+    scale = _out(scale, (fp8_blocks(N), fp8_blocks(K)), torch.float8_e8m0fnu, dev, stream, "scale")
+    check_same_device(W, codes, scale)
+    if not transposed:
+        _call("quantize_weights_fp8", dev, stream, W, dtype, N, K, codes, scale, None, None)
+        return codes, scale
+    codes_t = _empty((K, N), torch.float8_e4m3fn, dev, stream)
+    scale_t = _empty((fp8_blocks(K), fp8_blocks(N)), torch.float8_e8m0fnu, dev, stream)
+    _call("quantize_weights_fp8", dev, stream, W, dtype, N, K, codes, scale, codes_t if N else None,
+          scale_t if N else None)
+    return codes, scale, codes_t, scale_t
+
+
+def qlinear_fp8(a_codes, a_scale, w_codes, w_scale, out=None, stream=None):
+    """y[m, n] = sum_k (sa[m, k/128] qa[m, k]) (sw[n/128, k/128] qw[n, k]) as
+    bfloat16 [M, N], on the codes of quantize_fp8 and quantize_weights_fp8."""
+    import torch
+    M, K = _codes(a_codes, a_scale, 1, "a")
+    N, K2 = _codes(w_codes, w_scale, BLOCK, "w")
+    if K != K2:
+        raise ValueError("a_codes and w_codes disagree on K")
+    dev = check_same_device(a_codes, a_scale, w_codes, w_scale, out)
+    out = _out(out, (M, N), torch.bfloat16, dev, stream, "out")
+    _call("qlinear_fp8", dev, stream, a_codes, a_scale, w_codes, w_scale, M, N, K, out)
+    return out
+
+
+def qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype=None, out=None, stream=None):
+    """dW[n, k] = sum_m dY[m, n] (sa[m, k/128] qa[m, k]), the weight gradient
+    of qlinear_fp8 from the bfloat16 dY [M, N] and the codes kept of the
+    layer's input; bfloat16 (the default) or float32 [N, K].  N a multiple of 8."""
+    import torch
+    _matrix(dY, "dY", torch.bfloat16)
+    M, K = _codes(a_codes, a_scale, 1, "a")
+    N = dY.shape[1]
+    if dY.shape[0] != M:
+        raise ValueError("dY and a_codes disagree on the number of tokens")
+    if N:
+        check_fp8_width(N, "the width of dY", 8)
+    dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("the weight gradient is bfloat16 or float32")
+    dev = check_same_device(dY, a_codes, a_scale, out)
+    out = _out(out, (N, K), dtype, dev, stream, "out")
+    _call("qlinear_fp8_wgrad", dev, stream, dY, a_codes, a_scale, M, N, K, out, _dtype_code(out))
+    return out
+
+
+def gelu_backward_fp8(dH, x_codes, x_scale, quantize=False, out=None, stream=None):
+    """dX = dH * (Phi(x) + x phi(x)) as bfloat16 [T, d], the GELU's backward
+    pass from the 8-bit checkpoint of its input (quantize_fp8(...,
+    checkpoint=True)); dH bfloat16.
+
+    quantize=True also returns quantize_fp8(dX), for the product that follows:
+    (dX, codes, scale)."""
+    import torch
+    _matrix(dH, "dH", torch.bfloat16)
+    T, d = _codes(x_codes, x_scale, 1, "x")
+    _need_shape(dH, (T, d), "dH")
+    dev = check_same_device(dH, x_codes, x_scale, out)
+    out = _out(out, (T, d), torch.bfloat16, dev, stream, "out")
+    if not quantize:
+        _call("gelu_backward_fp8", dev, stream, dH, x_codes, x_scale, T, d, out, None, None)
+        return out
+    codes = _empty((T, d), torch.float8_e4m3fn, dev, stream)
+    scale = _empty((T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream)
+    _call("gelu_backward_fp8", dev, stream, dH, x_codes, x_scale, T, d, out, codes, scale)
+    return out, codes, scale
+
+
+_linear = None
+
+
+def _linear_function():
+    """The autograd function behind linear_fp8 (defined on first use: importing
+    the package does not import torch)."""
+    global _linear
+    if _linear is not None:
+        return _linear
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class LinearFP8(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W, activation):
+            need_x, need_w = ctx.needs_input_grad[:2]
+            x2 = X.reshape(-1, X.shape[-1]).contiguous()
+            gelu = _ACTS[activation] == RBQ_ACT_GELU
+            keep_x = gelu and need_x
+            aq, asc, *ck = quantize_fp8(x2, activation=activation, checkpoint=keep_x)
+            wq, wsc, *wt = quantize_weights_fp8(W.contiguous(), transposed=need_x)
+            y = qlinear_fp8(aq, asc, wq, wsc)
+            ctx.save_for_backward(*((aq, asc) if need_w else (None, None)), *(wt or (None, None)),
+                                  *(ck or (None, None)))
+            ctx.x_shape, ctx.x_dtype, ctx.w_dtype = X.shape, X.dtype, W.dtype
+            return y.view(*X.shape[:-1], W.shape[0])
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dY):
+            aq, asc, wt, wt_sc, xq, xsc = ctx.saved_tensors
+            dy2 = dY.reshape(-1, dY.shape[-1]).contiguous()
+            dX = dW = None
+            if ctx.needs_input_grad[0]:
+                dX = qlinear_fp8(*quantize_fp8(dy2), wt, wt_sc)
+                if xq is not None:
+                    dX = gelu_backward_fp8(dX, xq, xsc, out=dX)
+                dX = dX.view(ctx.x_shape).to(ctx.x_dtype)
+            if ctx.needs_input_grad[1]:
+                dW = qlinear_fp8_wgrad(dy2, aq, asc, dtype=ctx.w_dtype)
+            return dX, dW, None
+
+    _linear = LinearFP8
+    return _linear
+
+
+def linear_fp8(X, W, activation=None):
+    """act(X) W^T with both operands in block-scaled FP8: bfloat16 [..., N] from
+    X [..., K] and W [N, K] (bfloat16 or float32), act = identity or 'gelu'.
+
+    Differentiable in X and W.  What the backward pass needs is kept in 8
+    bits: the codes of act(X) for dW, of X for the GELU's slope, and of W^T for
+    dX (whose other operand, the incoming gradient, is quantised there).  W is
+    quantised in every call.  N and K multiples of 16."""
+    import torch
+    for t, name in ((X, "X"), (W, "W")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        _dtype_code(t)
+    if activation not in _ACTS:
+        raise ValueError("activation must be None, 'none' or 'gelu'")
+    if W.dim() != 2 or X.dim() < 1 or X.shape[-1] != W.shape[1]:
+        raise ValueError(f"X [..., K] and W [N, K] are wanted, got {tuple(X.shape)} and {tuple(W.shape)}")
+    check_fp8_width(W.shape[1], "K")
+    check_fp8_width(W.shape[0], "N")
+    check_same_device(X, W)
+    return _linear_function().apply(X, W, activation)

@@ -1,0 +1,65 @@
+// The block-scaled FP8 format of rbq_fp8_quant.cu, rbq_fp8_gemm.cu and
+// rbq_fp8_wgrad.cu: E4M3 codes with one power-of-two scale per block.
+//
+//   value = code * s,  s = 2^(b - 127),  b one byte (E8M0, as OCP MX names it)
+//   s = the smallest power of two with amax / s <= 448 (the largest E4M3
+//       value), and at least 2^-117; amax = the block's largest finite |x|.
+//
+// Why powers of two and not amax / 448 itself: the tensor cores multiply E8M0
+// scales in (tcgen05 kind::mxf8f6f4), so a scaled product costs what a plain
+// one does; x / s is exact, so a code carries one rounding and not two; and
+// code * s is exact in BF16 (4 significant bits), which is what the gradient
+// kernels feed their MMAs.  E4M3 is a floating-point format: up to the
+// binade of its subnormals the larger step between scales costs no accuracy.
+// The floor 2^-117 keeps every decoded value (down to 2^-9 s) a normal BF16
+// number; a block of zeros gets it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace rbq {
+namespace fp8 {
+
+constexpr int kBlock = 128;            // values per scale along a row (and rows per scale of a weight)
+constexpr int kMaxRows = 1 << 30;      // rows of an operand: tile coordinates stay in 32 bits
+constexpr uint32_t kMinScale = 10;     // 2^-117
+constexpr uint32_t kMaxScale = 247;    // 2^120: amax up to the largest fp32
+
+__host__ __device__ constexpr int blocks(int n) { return (n + kBlock - 1) / kBlock; }
+
+// E8M0 byte of a block whose largest finite magnitude is amax (>= 0): with
+// amax = m 2^(p - 127), 448 = 1.75 2^8, the exponent is p - 127 - 8, one more
+// when m > 1.75.
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int b = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(min(max(b, static_cast<int>(kMinScale)), static_cast<int>(kMaxScale)));
+}
+// 2^(127 - b), the factor from values to codes, and 2^(b - 127), for b in
+// [kMinScale, kMaxScale] both normal numbers.
+__device__ __forceinline__ float inv_scale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+// 2^(b - 127) for any byte: 0 is 2^-127 (a subnormal), 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  if (b == 0u) return __uint_as_float(0x00400000u);
+  return b == 255u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(b << 23);
+}
+
+// Four values -> four E4M3 bytes (round to nearest even; NaN -> 0x7F).
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+// Two E4M3 bytes -> two values.
+__device__ __forceinline__ float2 decode2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace fp8
+}  // namespace rbq

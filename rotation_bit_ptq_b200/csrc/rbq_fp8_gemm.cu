@@ -1,0 +1,745 @@
+// qlinear_fp8: the linear layer on block-scaled FP8 codes (format: rbq_fp8.cuh).
+//
+//   Y[m, n] = bf16( sum_k (sa[m, k/128] qa[m, k]) (sw[n/128, k/128] qw[n, k]) )
+//
+// on tcgen05 kind::mxf8f6f4 with block scales: the tensor core multiplies each
+// 32-value slice of K by the two operands' E8M0 scales, held in tensor memory,
+// and sums in fp32.  The hardware's block is 32 values, ours 128: the four MMAs
+// of a 128-value K slice use the same scale byte, and the four bytes of a
+// scale word hold four consecutive K slices (the instruction descriptor picks
+// the byte).  The product so runs at the rate of an unscaled FP8 product;
+// general fp32 scales would need every partial sum of 128 read back and
+// rescaled on the CUDA cores.
+//
+// Scales reach tensor memory through shared memory: four loader warps gather
+// the bytes (a row per thread; four K slices per 32-bit word) into the 32 x 16
+// byte blocks tcgen05.cp replicates over the four lane quadrants: the word of
+// row r at 16 (r % 32) + 4 (r / 32).
+//
+// Two kernels.
+// 1. fp8_pair_kernel (many tokens): persistent, on CTA pairs, 256 x 256 tiles
+//    (cta_group::2), K slices of 128, 6 stages of 32 KB per CTA.  Warps 0..3
+//    epilogue (one output row per thread), 4 MMA issuer, 5 TMA producer, 6..9
+//    scale loaders.  Two accumulators of 256 columns and the scales' 24 do not
+//    fit in the 512 columns of tensor memory, so the accumulators overlap in
+//    32 columns, which the epilogue reads first; the next tile's MMAs wait for
+//    that read only.
+// 2. fp8_few_kernel (few tokens): bound by reading the weights.  The weights
+//    take the MMA's M side (128 rows), the tokens its N side, and the CTAs of
+//    a cluster split K, each summing its part; the partial sums meet through
+//    distributed shared memory in a fixed order.
+//
+// Every mbarrier wait is bounded; a thread whose wait runs out raises a shared
+// abort flag, records an error in the library's device error word, and the
+// CTA still frees its TMEM.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include "rbq_fp8.cuh"
+#include "rbq_internal.h"
+#include "rbq_qcodes.cuh"
+#include "rbq_sm100.cuh"
+#include "rbq_tiles.cuh"
+
+namespace rbq {
+namespace fp8 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBK = 128;                  // K values (= bytes) per slice
+constexpr int kThreads = 320;             // 4 epilogue warps, MMA, TMA, 4 scale loader warps
+constexpr int kMmaWarp = 4, kTmaWarp = 5, kScaleWarp = 6;
+constexpr int kGroup = 4;                 // K slices per scale word
+constexpr int kSfBlock = 512;             // shared-memory bytes of 128 rows' scale words
+constexpr int kSfSlots = 4;               // ring of scale groups in shared memory
+
+// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (format 0), both
+// K-major, E8M0 scales (bit 23), N>>3 at bit 17, M>>4 at bit 24; bits 4-5 and
+// 29-30 pick the byte of B's and A's scale words.
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N) {
+  return (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_byte(uint32_t b) { return (b << 4) | (b << 29); }
+
+// D[tmem] (+)= (A scaled by sfa) (B scaled by sfb)^T.
+template <bool PAIR>
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows x 16 bytes of shared memory -> 4 columns of tensor memory, in every
+// lane quadrant (of both CTAs of a pair, each from its own shared memory).
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Shared-memory descriptor of a 32 x 16 byte scale block: no swizzle, groups
+// of 8 rows 128 bytes apart (stride offset), version 1.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1u) << 16) |
+         (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
+}
+
+// 32 bytes (eight words) to global memory in one store; dst 32-byte aligned.
+__device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// The scale bytes of K slices kb .. kb + 3 of one row of scales (kbs per row),
+// those past `end` as 0 (their codes are zero or not multiplied).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int end, bool vec) {
+  if (vec && kb + kGroup <= end) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (kb + j < end) w |= static_cast<uint32_t>(__ldg(row + kb + j)) << (8 * j);
+  return w;
+}
+__device__ __forceinline__ void put_scale_word(uint8_t* block, int r, uint32_t w) {
+  *reinterpret_cast<uint32_t*>(block + 16 * (r & 31) + 4 * (r >> 5)) = w;
+}
+
+struct Params {
+  int M, N, K, kbs;
+  const uint8_t* sa;          // [M, kbs]
+  const uint8_t* sw;          // [blocks(N), kbs]
+  uint16_t* Y;
+  unsigned int* err;
+  int order;                  // tile order (tiles::TileOrder)
+  int sf_vec;                 // scale rows readable as words (kbs % 4 == 0, aligned)
+  int y_vec;                  // 2: rows of Y 32-byte aligned, 1: 16-byte aligned, 0: neither
+};
+
+// ---- many tokens --------------------------------------------------------------
+constexpr int kBM = 128;                  // rows of A per CTA
+constexpr int kBN = 256;
+constexpr int kATile = kBM * kBK;         // 16 KB
+constexpr int kBTile = kBN / 2 * kBK;     // 16 KB: half of the tile's weight rows
+constexpr int kStage = kATile + kBTile;
+constexpr int kStages = 6;
+constexpr int kSfSlot = 3 * kSfBlock;     // 128 rows of A, 256 of B
+// Tensor memory: accumulator 0 in columns 0..255, accumulator 1 in 224..479,
+// two buffers of scales (4 columns of A, 8 of B) from 480.
+constexpr uint32_t kAcc1 = 224, kSfCol = 480, kSfCols = 12;
+
+struct __align__(8) Tail {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t sf_full[kSfSlots];
+  uint64_t sf_empty[kSfSlots];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t overlap;              // the shared columns of the last tile's accumulator have been read
+  uint64_t drain;                // abort path only: completion of the MMAs issued
+  uint32_t tmem_slot;
+  volatile uint32_t abort;
+};
+
+constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + sizeof(Tail) + 64;
+
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sf = ops + kStages * kStage;
+  Tail* tl = reinterpret_cast<Tail*>(sf + kSfSlots * kSfSlot);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int tile0 = static_cast<int>(cluster_id_x()), tstep = static_cast<int>(cluster_count_x());
+  const int ntiles_m = (p.M + 2 * kBM - 1) / (2 * kBM), ntiles_n = (p.N + kBN - 1) / kBN;
+  const int ntiles = ntiles_m * ntiles_n;
+  const int KS = p.kbs;
+  volatile uint32_t* abort = &tl->abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&tl->full[s], 1);
+      mbar_init(&tl->empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&tl->sf_full[s], 8);       // one arrival per loader warp of both CTAs
+      mbar_init(&tl->sf_empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tl->acc_full[a], 1);
+      mbar_init(&tl->acc_empty[a], 8);     // one arrival per epilogue warp of both CTAs
+    }
+    mbar_init(&tl->overlap, 8);
+    mbar_init(&tl->drain, 1);
+    tl->abort = 0u;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(&tl->tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();                          // a pair's barriers are signalled from both CTAs
+  tc_fence_after();
+  const uint32_t tmem = tl->tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == kMmaWarp) {
+    // ---------------- MMA issuer (the even CTA's) ----------------
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t kIdesc = idesc_mx(2 * kBM, kBN);
+      const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
+      const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
+      uint32_t s = 0, ph = 0, it = 0, g = 0;     // operand stage, its phase; tile; scale group
+      bool ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++it) {
+        const uint32_t a = it & 1u, use = it >> 1;
+        if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
+        if (it >= 1 && !mbar_wait_or_abort_cl(&tl->overlap, (it - 1) & 1, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t acc = tmem + a * kAcc1;
+        uint32_t sfa = 0;
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t j = ks & (kGroup - 1);
+          if (j == 0) {
+            const uint32_t slot = g % kSfSlots;
+            // the MMAs that read this buffer's last contents (group g - 2) have completed
+            if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            if (!mbar_wait_or_abort_cl(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
+            tc_fence_after();
+            sfa = tmem + kSfCol + (g & 1u) * kSfCols;
+            const uint64_t sd = sfdesc0 + ((slot * kSfSlot) >> 4);
+            cp_scales<true>(sfa, sd);
+            cp_scales<true>(sfa + 4, sd + (kSfBlock >> 4));
+            cp_scales<true>(sfa + 8, sd + (2 * kSfBlock >> 4));
+          }
+          if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kStage)) >> 4);
+          const uint64_t bd = ad + (kATile >> 4);
+          const uint32_t id = kIdesc | idesc_byte(j);
+          umma_mx<true>(acc, ad, bd, id, sfa, sfa + 4, ks != 0);
+          umma_mx<true>(acc, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);     // +32 bytes = 32 values of K
+          umma_mx<true>(acc, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
+          umma_mx<true>(acc, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
+          umma_commit_pair(&tl->empty[s], 3);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+          if (j == kGroup - 1 || ks == KS - 1) {
+            umma_commit_pair(&tl->sf_empty[g % kSfSlots], 3);
+            ++g;
+          }
+        }
+        if (ok) umma_commit_pair(&tl->acc_full[a], 3);
+      }
+      if (!ok) atomicOr(p.err, 2u);
+    }
+  } else if (warp == kTmaWarp) {
+    // ---------------- TMA producer: each CTA its own rows, both CTAs' bytes on the even CTA's barrier ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      uint32_t s = 0, ph = 0;
+      bool first = true, ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+        int mt, nt;
+        tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
+        const int m0 = mt * 2 * kBM + static_cast<int>(rank) * kBM;
+        const int n0 = nt * kBN + static_cast<int>(rank) * (kBN / 2);
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!first && !mbar_wait_or_abort(&tl->empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          uint8_t* st = ops + s * kStage;
+          if (rank == 0) mbar_arrive_expect_tx(&tl->full[s], 2 * kStage);
+          const uint32_t bar = mapa_shared(&tl->full[s], 0);
+          tma_load_2d_pair(st, &tmA, ks * kBK, m0, bar);
+          tma_load_2d_pair(st + kATile, &tmB, ks * kBK, n0, bar);
+          if (++s == kStages) { s = 0; ph ^= 1u; first = false; }
+        }
+      }
+      if (!ok) atomicOr(p.err, 16u);
+    }
+  } else if (warp >= kScaleWarp) {
+    // ---------------- scale loaders: this CTA's 128 rows of A, all 256 of B ----------------
+    const int r = tid - 32 * kScaleWarp;
+    const int last_nb = blocks(p.N) - 1;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+      int mt, nt;
+      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
+      const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r;
+      const uint8_t* ra = p.sa + static_cast<long long>(m) * p.kbs;
+      const int nb = nt * (kBN / kBlock);
+      const uint8_t* rb0 = p.sw + static_cast<long long>(nb) * p.kbs;
+      const uint8_t* rb1 = p.sw + static_cast<long long>(min(nb + 1, last_nb)) * p.kbs;
+      for (int kb = 0; kb < p.kbs; kb += kGroup, ++g) {
+        const uint32_t wa = m < p.M ? scale_word(ra, kb, p.kbs, p.sf_vec) : 0u;
+        const uint32_t wb0 = scale_word(rb0, kb, p.kbs, p.sf_vec), wb1 = scale_word(rb1, kb, p.kbs, p.sf_vec);
+        const uint32_t slot = g % kSfSlots, use = g / kSfSlots;
+        if (use >= 1 && !mbar_warp_wait(&tl->sf_empty[slot], (use - 1) & 1, abort)) { ok = false; break; }
+        uint8_t* blk = sf + slot * kSfSlot;
+        put_scale_word(blk, r, wa);
+        put_scale_word(blk + kSfBlock, r, wb0);
+        put_scale_word(blk + 2 * kSfBlock, r, wb1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->sf_full[slot], 0));
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.err, 32u);
+  } else {
+    // ---------------- epilogue ----------------
+    const int r = 32 * warp + lane;         // row within this CTA's 128 rows of the tile
+    uint32_t it = 0;
+    for (int tile = tile0; tile < ntiles; tile += tstep, ++it) {
+      const uint32_t a = it & 1u, use = it >> 1;
+      if (!mbar_warp_wait(&tl->acc_full[a], use & 1, abort)) {   // warp-uniform: tmem loads follow
+        if (lane == 0) atomicOr(p.err, 4u);
+        break;
+      }
+      tc_fence_after();
+      int mt, nt;
+      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
+      const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r;
+      const uint32_t tq = tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * kAcc1;
+#pragma unroll 1
+      for (int c = 0; c < kBN / 32; ++c) {
+        const int cc = a == 0 ? kBN / 32 - 1 - c : c;   // the columns both accumulators share come first
+        uint32_t v[32];
+        tmem_ld32(tq + 32 * cc, v);
+        tmem_wait_ld();
+        if (c == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->overlap, 0));
+        }
+        const int nb = nt * kBN + 32 * cc;
+        if (m >= p.M || nb >= p.N) continue;
+        uint16_t* dst = p.Y + static_cast<long long>(m) * p.N + nb;
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if (nb + 32 <= p.N && p.y_vec == 2) {
+          st_v8(dst, o);
+          st_v8(dst + 16, o + 8);
+        } else if (nb + 32 <= p.N && p.y_vec == 1) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (nb + j < p.N) dst[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->acc_empty[a], 0));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tl->abort) {                 // the same value in every thread after the barrier
+    drain_after_abort(warp == kMmaWarp && lane == 0 && rank == 0, &tl->drain, true);
+    __syncthreads();
+  }
+  // Neither CTA of a pair leaves while the other may still signal its
+  // barriers or the MMAs may still read its shared memory.
+  cluster_sync();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---- few tokens ----------------------------------------------------------------
+// Tile: 128 output columns (weight rows) x NT tokens; the S CTAs of a cluster
+// take consecutive parts of the K slices.
+template <int NT>
+struct Few {
+  static constexpr int kWTile = kBM * kBK;                       // 16 KB of weights
+  static constexpr int kTTile = NT * kBK;
+  static constexpr int kStage = kWTile + kTTile;
+  static constexpr int kStages = (NT <= 64 ? 8 : NT == 128 ? 6 : 4);
+  static constexpr int kSfSlot = kSfBlock * (NT > 128 ? 3 : 2);
+  static constexpr uint32_t kSfCol = NT, kSfCols = NT > 128 ? 12 : 8;     // columns of a scale buffer
+  static constexpr uint32_t kTmemCols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT == 64 ? 128 : NT == 128 ? 256 : 512;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr size_t kSmem = 1024 + kRing + kSfSlots * kSfSlot + 512;
+  static_assert(kSfCol + 2 * kSfCols <= kTmemCols, "accumulator and scales fit");
+  static_assert(NT * kBM * 4 <= kRing, "the partial sums fit where the operands were");
+};
+
+struct __align__(8) FewTail {
+  uint64_t full[8];
+  uint64_t empty[8];
+  uint64_t sf_full[kSfSlots];
+  uint64_t sf_empty[kSfSlots];
+  uint64_t acc_full;
+  uint64_t drain;
+  uint32_t tmem_slot;
+  volatile uint32_t abort;
+};
+static_assert(sizeof(FewTail) <= 512, "the tail fits");
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT, const Params p) {
+  using F = Few<NT>;
+  constexpr int kS = F::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sf = ops + F::kRing;
+  FewTail* tl = reinterpret_cast<FewTail*>(sf + kSfSlots * F::kSfSlot);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t rank, S;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  const int ntiles_n = blocks(p.N);
+  const int tile = static_cast<int>(cluster_id_x());
+  const int nt = tile % ntiles_n, mt = tile / ntiles_n;
+  const int n0 = nt * kBM, m0 = mt * NT;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.kbs) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.kbs) * (rank + 1) / S);   // S <= kbs: never empty
+  volatile uint32_t* abort = &tl->abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(&tl->full[s], 1);
+      mbar_init(&tl->empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&tl->sf_full[s], 4);
+      mbar_init(&tl->sf_empty[s], 1);
+    }
+    mbar_init(&tl->acc_full, 1);
+    mbar_init(&tl->drain, 1);
+    tl->abort = 0u;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tl->tmem_slot, F::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tl->tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_mx(kBM, NT);
+      const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
+      const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
+      uint32_t s = 0, ph = 0, g = 0, sfa = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t j = (kb - kb0) & (kGroup - 1);
+        if (j == 0) {
+          const uint32_t slot = g % kSfSlots;
+          if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait_or_abort(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
+          tc_fence_after();
+          sfa = tmem + F::kSfCol + (g & 1u) * F::kSfCols;
+          const uint64_t sd = sfdesc0 + ((slot * F::kSfSlot) >> 4);
+          cp_scales<false>(sfa, sd);
+          cp_scales<false>(sfa + 4, sd + (kSfBlock >> 4));
+          if constexpr (NT > 128) cp_scales<false>(sfa + 8, sd + (2 * kSfBlock >> 4));
+        }
+        if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(F::kStage)) >> 4);
+        const uint64_t bd = ad + (F::kWTile >> 4);
+        const uint32_t id = kIdesc | idesc_byte(j);
+        umma_mx<false>(tmem, ad, bd, id, sfa, sfa + 4, kb != kb0);
+        umma_mx<false>(tmem, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);
+        umma_mx<false>(tmem, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
+        umma_mx<false>(tmem, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
+        umma_commit(&tl->empty[s]);
+        if (++s == kS) { s = 0; ph ^= 1u; }
+        if (j == kGroup - 1 || kb == kb1 - 1) {
+          umma_commit(&tl->sf_empty[g % kSfSlots]);
+          ++g;
+        }
+      }
+      if (ok)
+        umma_commit(&tl->acc_full);
+      else
+        atomicOr(p.err, 2u);
+    }
+  } else if (warp == kTmaWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmT);
+      uint32_t s = 0, ph = 0;
+      bool first = true, ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!first && !mbar_wait_or_abort(&tl->empty[s], ph ^ 1u, abort)) { ok = false; break; }
+        uint8_t* st = ops + s * F::kStage;
+        mbar_arrive_expect_tx(&tl->full[s], F::kStage);
+        tma_load_2d(st, &tmW, kb * kBK, n0, &tl->full[s]);
+        tma_load_2d(st + F::kWTile, &tmT, kb * kBK, m0, &tl->full[s]);
+        if (++s == kS) { s = 0; ph ^= 1u; first = false; }
+      }
+      if (!ok) atomicOr(p.err, 16u);
+    }
+  } else if (warp >= kScaleWarp) {
+    const int r = tid - 32 * kScaleWarp;
+    const uint8_t* rw = p.sw + static_cast<long long>(nt) * p.kbs;
+    const uint8_t* rt0 = p.sa + static_cast<long long>(m0 + r) * p.kbs;
+    const uint8_t* rt1 = rt0 + 128ll * p.kbs;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; kb += kGroup, ++g) {
+      const bool vec = p.sf_vec && (kb & 3) == 0;
+      const uint32_t ww = scale_word(rw, kb, kb1, vec);
+      const uint32_t w0 = r < NT && m0 + r < p.M ? scale_word(rt0, kb, kb1, vec) : 0u;
+      const uint32_t w1 = NT > 128 && m0 + r + 128 < p.M ? scale_word(rt1, kb, kb1, vec) : 0u;
+      const uint32_t slot = g % kSfSlots, use = g / kSfSlots;
+      if (use >= 1 && !mbar_warp_wait(&tl->sf_empty[slot], (use - 1) & 1, abort)) { ok = false; break; }
+      uint8_t* blk = sf + slot * F::kSfSlot;
+      put_scale_word(blk, r, ww);
+      put_scale_word(blk + kSfBlock, r, w0);
+      if constexpr (NT > 128) put_scale_word(blk + 2 * kSfBlock, r, w1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tl->sf_full[slot]);
+    }
+    if (!ok && lane == 0) atomicOr(p.err, 32u);
+  } else {
+    // partial sums -> red[token][128 columns] where the operands were: every
+    // slice has been loaded and multiplied once acc_full completes
+    float* red = reinterpret_cast<float*>(ops);
+    if (mbar_warp_wait(&tl->acc_full, 0, abort)) {
+      tc_fence_after();
+      constexpr int kStep = NT < 32 ? 16 : 32;
+#pragma unroll 1
+      for (int c = 0; c < NT && m0 + c < p.M; c += kStep) {
+        uint32_t v[32];
+        if constexpr (kStep == 32)
+          tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, v);
+        else
+          tmem_ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) red[(c + j) * kBM + 32 * warp + lane] = __uint_as_float(v[j]);
+      }
+    } else if (lane == 0) {
+      atomicOr(p.err, 4u);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  const bool failed = tl->abort != 0u;
+  if (failed) {
+    drain_after_abort(warp == kMmaWarp && lane == 0, &tl->drain);
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, F::kTmemCols);
+  }
+  // the cluster's partial sums, added in the order of their K slices; CTA
+  // `rank` finishes tokens rank, rank + S, ...
+  if (S > 1) cluster_sync();
+  const int tokens = min(NT, p.M - m0);
+  if (tid < 256) {
+    const int n = tid & 127;
+    const uint32_t mine = smem_u32(ops) + 4u * n;
+    if (n0 + n < p.N) {
+      for (int t = static_cast<int>(rank) + static_cast<int>(S) * (tid >> 7); t < tokens; t += 2 * static_cast<int>(S)) {
+        float sum = 0.f;
+        for (uint32_t c = 0; c < S; ++c) {
+          uint32_t addr;
+          float v;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(mine + 4u * kBM * t), "r"(c));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+          sum += v;
+        }
+        p.Y[static_cast<long long>(m0 + t) * p.N + n0 + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+      }
+    }
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync();       // no CTA leaves while another reads its sums
+}
+
+// uint8 [rows, K] K-major, boxes of box_rows x 128 bytes, 128B swizzle.
+int encode_map(CUtensorMap* map, const uint8_t* base, int rows, int K, int box_rows) {
+  auto fn = qfast::encode_fn();
+  if (!fn) return RBQ_ECUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
+}
+
+cudaLaunchAttribute cluster_attr(int size) {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = size;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+cudaLaunchAttribute pdl_attr() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
+// Pairs of the pair kernel that can be resident on device `dev`, asked once per device (0: none).
+int pair_clusters(int dev) {
+  static int cached[kMaxDevices] = {};        // 0 = not yet asked; else pairs + 1
+  if (cached[dev]) return cached[dev] - 1;
+  if (cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1] = {cluster_attr(2)};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cached[dev] = n + 1;
+  return n;
+}
+
+int launch_pair(const uint8_t* a, const uint8_t* w, Params p, int dev, cudaStream_t st) {
+  int clusters = pair_clusters(dev);
+  if (clusters < 1) return RBQ_ECUDA;
+  p.order = tiles::tile_order(dev, 1LL * p.M * p.K, 1LL * p.N * p.K);
+  CUtensorMap mA, mB;
+  int rc = encode_map(&mA, a, p.M, p.K, kBM);
+  if (rc != RBQ_OK) return rc;
+  if ((rc = encode_map(&mB, w, p.N, p.K, kBN / 2)) != RBQ_OK) return rc;
+  const long long ntiles = ((p.M + 2LL * kBM - 1) / (2 * kBM)) * ((p.N + kBN - 1) / kBN);
+  if (ntiles > 0x7FFFFFFFll) return RBQ_EINVAL;
+  if (clusters > ntiles) clusters = static_cast<int>(ntiles);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * clusters, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2] = {pdl_attr(), cluster_attr(2)};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel, mA, mB, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+}
+
+template <int NT>
+int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int dev, int sms, cudaStream_t st) {
+  using F = Few<NT>;
+  static bool ready[kMaxDevices] = {};
+  if (!ready[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(fp8_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(F::kSmem));
+    if (e != cudaSuccess) return cuda_fail(e);
+    ready[dev] = true;
+  }
+  const long long ntiles = static_cast<long long>(blocks(p.N)) * ((p.M + NT - 1) / NT);
+  // K split over a cluster while the SMs are not all in use and each part keeps two slices or more
+  int S = 1;
+  while (S < 8 && ntiles * S * 2 <= sms && p.kbs >= 4 * S) S *= 2;
+  if (ntiles * S > 0x7FFFFFFFll) return RBQ_EINVAL;
+  CUtensorMap mW, mT;
+  int rc = encode_map(&mW, w, p.N, p.K, kBM);
+  if (rc != RBQ_OK) return rc;
+  if ((rc = encode_map(&mT, a, p.M, p.K, NT)) != RBQ_OK) return rc;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ntiles * S), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2] = {pdl_attr(), cluster_attr(S)};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_few_kernel<NT>, mW, mT, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace fp8
+}  // namespace rbq
+
+using namespace rbq;
+
+extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                           const uint8_t* w_scales, int M, int N, int K, uint16_t* Y, void* stream) {
+  if (M < 0 || M > fp8::kMaxRows || N < 0 || N > fp8::kMaxRows || K <= 0 || K % 16) return RBQ_EINVAL;
+  if (M == 0 || N == 0) return RBQ_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return RBQ_EINVAL;
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(Y, 2)) return RBQ_EALIGN;
+  fp8::Params p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.kbs = fp8::blocks(K);
+  p.sa = a_scales;
+  p.sw = w_scales;
+  p.Y = Y;
+  p.sf_vec = p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4);
+  p.y_vec = N % 16 == 0 && aligned(Y, 32) ? 2 : N % 8 == 0 && aligned(Y, 16) ? 1 : 0;
+  int rc = device_error_word_ptr(&p.err);
+  if (rc != RBQ_OK) return rc;
+  int dev = 0, sms = 148;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M <= 16) return fp8::launch_few<16>(a_codes, w_codes, p, dev, sms, st);
+  if (M <= 32) return fp8::launch_few<32>(a_codes, w_codes, p, dev, sms, st);
+  if (M <= 64) return fp8::launch_few<64>(a_codes, w_codes, p, dev, sms, st);
+  if (M <= 128) return fp8::launch_few<128>(a_codes, w_codes, p, dev, sms, st);
+  if (M <= 256) return fp8::launch_few<256>(a_codes, w_codes, p, dev, sms, st);
+  return fp8::launch_pair(a_codes, w_codes, p, dev, st);
+}

@@ -1,0 +1,447 @@
+// qlinear_fp8_wgrad: the weight gradient of a linear layer from the 8-bit
+// codes kept of its input (format: rbq_fp8.cuh).
+//
+//   dW[n, k] = sum_m dY[m, n] x[m, k],   x[m, k] = code[m, k] 2^(b[m, k/128] - 127)
+//
+// The sum runs over tokens, and the scales change from token to token along
+// it, so they cannot be taken out of the product; but code * scale is exact in
+// BF16, so the product runs on BF16 operands (tcgen05 kind::f16, fp32 sums)
+// with no rounding besides dY's own.
+//
+// Two kernels per call (three when the tokens are split):
+// 1. decode_rows_kernel: codes and scales -> BF16 [M, K] in a stream-ordered
+//    workspace.
+// 2. wgrad_kernel: persistent, on CTA pairs, 256 x 256 tiles of dW
+//    (cta_group::2), slices of 64 tokens.  Both operands lie with the token
+//    as their row, so they are "MN-major": a TMA box of 64 tokens x 64
+//    columns (128 bytes, 128B swizzle) is one column of swizzle atoms.  Warps
+//    0..3 epilogue, 4 MMA issuer, 5 TMA producer.
+// 3. With too few tiles to fill the GPU the tokens are split: each part's sums
+//    go to the workspace in fp32 and sum_parts_kernel adds them in order.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include "rbq_fp8.cuh"
+#include "rbq_internal.h"
+#include "rbq_qcodes.cuh"
+#include "rbq_sm100.cuh"
+#include "rbq_tiles.cuh"
+
+namespace rbq {
+namespace fp8 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTok = 64;                   // tokens per slice
+constexpr int kTile = 256;                 // rows and columns of dW per tile
+constexpr int kHalf = 128;                 // of them per CTA and operand
+constexpr int kBox = 64;                   // columns per TMA box (128 bytes)
+constexpr int kBoxBytes = kBox * 2 * kTok; // 8 KB
+constexpr int kOperand = kHalf / kBox * kBoxBytes;   // 16 KB
+constexpr int kWStage = 2 * kOperand;
+constexpr int kWStages = 6;
+constexpr int kWThreads = 192;
+constexpr int kWMmaWarp = 4, kWTmaWarp = 5;
+
+// Instruction descriptor: BF16 A and B, both MN-major (bits 15 and 16), fp32 sums.
+constexpr uint32_t kWIdesc = idesc_f16(kTile, kTile, true) | (1u << 15) | (1u << 16);
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle
+// layout: 64 columns x 8 tokens per swizzle atom; the next 8 tokens 1024
+// bytes on (stride offset), the next 64 columns one box on (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
+         (static_cast<uint64_t>(2u) << 61);
+}
+
+struct WParams {
+  int M, N, K;
+  void* out;                  // [N, K] BF16 or fp32, or [parts, N, K] fp32
+  int f32;
+  int parts;                  // token ranges, each summed apart
+  int out_vec;                // rows of `out` 32-byte aligned
+  int order;
+  unsigned int* err;
+};
+
+struct __align__(8) WTail {
+  uint64_t full[kWStages];
+  uint64_t empty[kWStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_slot;
+  volatile uint32_t abort;
+};
+
+constexpr size_t kWSmem = 1024 + kWStages * kWStage + sizeof(WTail) + 64;
+
+__device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Slices [first, last) of part `part`.
+__device__ __forceinline__ void part_range(int slices, int parts, int part, int& first, int& last) {
+  first = static_cast<int>(static_cast<long long>(slices) * part / parts);
+  last = static_cast<int>(static_cast<long long>(slices) * (part + 1) / parts);
+}
+
+__global__ void __launch_bounds__(kWThreads, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX, const WParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  WTail* tl = reinterpret_cast<WTail*>(ops + kWStages * kWStage);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int work0 = static_cast<int>(cluster_id_x()), wstep = static_cast<int>(cluster_count_x());
+  const int ntiles_n = (p.N + kTile - 1) / kTile, ntiles_k = (p.K + kTile - 1) / kTile;
+  const int ntiles = ntiles_n * ntiles_k, nwork = ntiles * p.parts;
+  const int slices = (p.M + kTok - 1) / kTok;
+  volatile uint32_t* abort = &tl->abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < kWStages; ++s) {
+      mbar_init(&tl->full[s], 1);
+      mbar_init(&tl->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tl->acc_full[a], 1);
+      mbar_init(&tl->acc_empty[a], 8);
+    }
+    mbar_init(&tl->drain, 1);
+    tl->abort = 0u;
+    mbar_fence_init();
+  }
+  if (warp == kWMmaWarp) {
+    tmem_alloc_pair(&tl->tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tl->tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == kWMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      const uint64_t desc0 = sdesc_mn_sw128(smem_u32(ops));
+      uint32_t s = 0, ph = 0, it = 0;
+      bool ok = true;
+      for (int w = work0; w < nwork && ok; w += wstep, ++it) {
+        const uint32_t a = it & 1u, use = it >> 1;
+        if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t acc = tmem + a * kTile;
+        int first, last;
+        part_range(slices, p.parts, w / ntiles, first, last);
+        for (int t = first; t < last; ++t) {
+          if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kWStage)) >> 4);
+          const uint64_t bd = ad + (kOperand >> 4);
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)          // 16 tokens = two atoms of 8
+            umma_f16_pair(acc, ad + k * (2048 >> 4), bd + k * (2048 >> 4), kWIdesc, t != first || k != 0);
+          umma_commit_pair(&tl->empty[s], 3);
+          if (++s == kWStages) { s = 0; ph ^= 1u; }
+        }
+        if (ok) umma_commit_pair(&tl->acc_full[a], 3);
+      }
+      if (!ok) atomicOr(p.err, 2u);
+    }
+  } else if (warp == kWTmaWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmY);
+      tma_prefetch_desc(&tmX);
+      uint32_t s = 0, ph = 0;
+      bool wrapped = false, ok = true;
+      for (int w = work0; w < nwork && ok; w += wstep) {
+        int nt, kt, first, last;
+        tiles::tile_coords(w % ntiles, ntiles_n, ntiles_k, p.order, nt, kt);
+        part_range(slices, p.parts, w / ntiles, first, last);
+        const int n0 = nt * kTile + static_cast<int>(rank) * kHalf, k0 = kt * kTile + static_cast<int>(rank) * kHalf;
+        for (int t = first; t < last; ++t) {
+          if (wrapped && !mbar_wait_or_abort(&tl->empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          uint8_t* st = ops + s * kWStage;
+          if (rank == 0) mbar_arrive_expect_tx(&tl->full[s], 2 * kWStage);
+          const uint32_t bar = mapa_shared(&tl->full[s], 0);
+#pragma unroll
+          for (int b = 0; b < kHalf / kBox; ++b) {
+            tma_load_2d_pair(st + b * kBoxBytes, &tmY, n0 + b * kBox, t * kTok, bar);
+            tma_load_2d_pair(st + kOperand + b * kBoxBytes, &tmX, k0 + b * kBox, t * kTok, bar);
+          }
+          if (++s == kWStages) { s = 0; ph ^= 1u; wrapped = true; }
+        }
+      }
+      if (!ok) atomicOr(p.err, 16u);
+    }
+  } else {
+    const int r = 32 * warp + lane;
+    uint32_t it = 0;
+    for (int w = work0; w < nwork; w += wstep, ++it) {
+      const uint32_t a = it & 1u, use = it >> 1;
+      if (!mbar_warp_wait(&tl->acc_full[a], use & 1, abort)) {
+        if (lane == 0) atomicOr(p.err, 4u);
+        break;
+      }
+      tc_fence_after();
+      int nt, kt;
+      tiles::tile_coords(w % ntiles, ntiles_n, ntiles_k, p.order, nt, kt);
+      const int n = nt * kTile + static_cast<int>(rank) * kHalf + r;
+      const long long row = static_cast<long long>(w / ntiles) * p.N + n;
+#pragma unroll 1
+      for (int cc = 0; cc < kTile / 32; ++cc) {
+        uint32_t v[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * kTile + 32 * cc, v);
+        tmem_wait_ld();
+        const int kc = kt * kTile + 32 * cc;
+        if (n >= p.N || kc >= p.K) continue;
+        const int left = p.K - kc;                      // a multiple of 16
+        if (p.f32) {
+          float* dst = static_cast<float*>(p.out) + row * p.K + kc;
+          if (p.out_vec) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (8 * j < left) st_v8(dst + 8 * j, v + 8 * j);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < left) dst[j] = __uint_as_float(v[j]);
+          }
+        } else {
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.K + kc;
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (p.out_vec) {
+            st_v8(dst, o);
+            if (left > 16) st_v8(dst + 16, o + 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < left) dst[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->acc_empty[a], 0));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tl->abort) {
+    drain_after_abort(warp == kWMmaWarp && lane == 0 && rank == 0, &tl->drain, true);
+    __syncthreads();
+  }
+  cluster_sync();
+  if (warp == kWMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Codes and scales -> BF16 values, 16 per thread (K is a multiple of 16).
+__global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, const uint8_t* scales, long long pieces,
+                                                          int K, int kbs, uint16_t* out) {
+  const int per_row = K / 16;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < pieces; i += 256ll * gridDim.x) {
+    const long long row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 16;
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+    const float s = scale_value(__ldg(scales + row * kbs + col / kBlock));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = decode2(w[j / 2] >> (16 * (j & 1)));
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v.x * s, v.y * s);      // exact
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + 16 * i);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// out[i] = part 0 + part 1 + ... in that order.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int nparts, long long n4, void* out,
+                                                        int f32) {
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += 256ll * gridDim.x) {
+    float4 s = parts[i];
+    for (int q = 1; q < nparts; ++q) {
+      const float4 v = parts[q * n4 + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    if (f32) {
+      static_cast<float4*>(out)[i] = s;
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+      static_cast<uint2*>(out)[i] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  }
+}
+
+// BF16 [rows, cols] row-major, boxes of 64 rows (tokens) x 64 columns, 128B swizzle.
+int encode_tokens_map(CUtensorMap* map, const uint16_t* base, int rows, int cols) {
+  auto fn = qfast::encode_fn();
+  if (!fn) return RBQ_ECUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {2 * static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBox), static_cast<cuuint32_t>(kTok)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
+}
+
+// Pairs of wgrad_kernel that can be resident on device `dev`, asked once per device (0: none).
+int wgrad_pairs(int dev) {
+  static int cached[kMaxDevices] = {};        // 0 = not yet asked; else pairs + 1
+  if (cached[dev]) return cached[dev] - 1;
+  if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kWSmem)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kWThreads, 1, 1);
+  cfg.dynamicSmemBytes = kWSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, wgrad_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cached[dev] = n + 1;
+  return n;
+}
+
+int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M, int N, int K, void* dW, bool f32,
+          unsigned int* err, cudaStream_t st) {
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int pairs = wgrad_pairs(dev);
+  if (pairs < 1) return RBQ_ECUDA;
+  const long long ntiles = ((N + kTile - 1LL) / kTile) * ((K + kTile - 1LL) / kTile);
+  if (ntiles > (1 << 24)) return RBQ_EINVAL;
+  const int slices = (M + kTok - 1) / kTok;
+  int parts = 1;
+  while (ntiles * (parts + 1) <= pairs && slices >= 4 * (parts + 1)) ++parts;
+
+  cudaMemPool_t pool = qfast::workspace_pool(dev);
+  if (!pool) return RBQ_ECUDA;
+  const size_t x_bytes = (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256;
+  const size_t part_bytes = parts > 1 ? static_cast<size_t>(parts) * N * K * 4 : 0;
+  void* ws = nullptr;
+  e = cudaMallocFromPoolAsync(&ws, x_bytes + part_bytes, pool, st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  uint16_t* x = static_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + x_bytes);
+
+  const long long pieces = static_cast<long long>(M) * (K / 16);
+  long long grid = (pieces + 255) / 256;
+  if (grid > 16LL * sms) grid = 16LL * sms;
+  decode_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(codes, scales, pieces, K, blocks(K), x);
+  e = cudaGetLastError();
+  int rc = e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+
+  WParams p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.parts = parts;
+  p.f32 = parts > 1 || f32;
+  p.out = parts > 1 ? part : dW;
+  p.out_vec = parts > 1 || aligned(dW, 32);      // rows are multiples of 16 values
+  p.order = tiles::tile_order(dev, 2LL * M * N, 2LL * M * K);
+  p.err = err;
+  CUtensorMap mY, mX;
+  if (rc == RBQ_OK) rc = encode_tokens_map(&mY, dY, M, N);
+  if (rc == RBQ_OK) rc = encode_tokens_map(&mX, x, M, K);
+  if (rc == RBQ_OK) {
+    const long long nwork = ntiles * parts;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(nwork < pairs ? nwork : pairs), 1, 1);
+    cfg.blockDim = dim3(kWThreads, 1, 1);
+    cfg.dynamicSmemBytes = kWSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, wgrad_kernel, mY, mX, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) rc = cuda_fail(e);
+  }
+  if (rc == RBQ_OK && parts > 1) {
+    const long long n4 = static_cast<long long>(N) * K / 4;
+    long long g = (n4 + 255) / 256;
+    if (g > 16LL * sms) g = 16LL * sms;
+    sum_parts_kernel<<<static_cast<unsigned>(g), 256, 0, st>>>(reinterpret_cast<const float4*>(part), parts, n4, dW,
+                                                               f32);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) rc = cuda_fail(e);
+  }
+  e = cudaFreeAsync(ws, st);
+  if (rc == RBQ_OK && e != cudaSuccess) rc = cuda_fail(e);
+  return rc;
+}
+
+}  // namespace
+}  // namespace fp8
+}  // namespace rbq
+
+using namespace rbq;
+
+extern "C" int qlinear_fp8_wgrad(const uint16_t* dY, const uint8_t* a_codes, const uint8_t* a_scales, int M, int N,
+                                 int K, void* dW, int dtype, void* stream) {
+  if (M < 0 || M > fp8::kMaxRows || N < 0 || N > fp8::kMaxRows || N % 8 || K <= 0 || K % 16) return RBQ_EINVAL;
+  if (dtype != RBQ_BF16 && dtype != RBQ_F32) return RBQ_EINVAL;
+  if (N == 0) return RBQ_OK;
+  if (!dW) return RBQ_EINVAL;
+  if (!aligned(dW, 16)) return RBQ_EALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {                                   // no tokens: a gradient of zeros
+    const cudaError_t e = cudaMemsetAsync(dW, 0, static_cast<size_t>(N) * K * (dtype == RBQ_F32 ? 4 : 2), st);
+    return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+  }
+  if (!dY || !a_codes || !a_scales) return RBQ_EINVAL;
+  if (!aligned(dY, 16) || !aligned(a_codes, 16)) return RBQ_EALIGN;
+  unsigned int* err = nullptr;
+  const int rc = device_error_word_ptr(&err);
+  if (rc != RBQ_OK) return rc;
+  return fp8::wgrad(dY, a_codes, a_scales, M, N, K, dW, dtype == RBQ_F32, err, st);
+}
