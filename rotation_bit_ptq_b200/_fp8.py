@@ -8,7 +8,8 @@ Codes are torch.float8_e4m3fn and scales torch.float8_e8m0fnu tensors, so
 
 import contextlib
 
-from . import (RBQ_ACT_GELU, RBQ_ACT_NONE, _ACTS, _check, _dtype_code, _need_cuda, _need_shape, check_same_device, lib)
+from . import (RBQ_ACT_GELU, RBQ_ACT_NONE, RBQ_BF16, RBQ_F32, _ACTS, _check, _dtype_code, _need_cuda, _need_shape,
+               check_same_device, lib)
 
 BLOCK = 128
 
@@ -35,50 +36,79 @@ def _on(device, stream):
             yield
 
 
-def _call(name, device, stream, *args):
-    """lib().name(*args, stream) with `device` current; tensors go as pointers."""
-    import torch
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    fn = getattr(lib(), name)
-    if stream is None and torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with _on(device, stream):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(rc, name)
+# The checks of an ordinary call cost more than its launch if each asks torch
+# for objects (devices, streams, shapes as tuples): a single token's product
+# took 15.9 us of host time that way and takes 9 us with the plain integers
+# and singletons used here.  What fails them goes through the slower checks,
+# which word the error.
 
-
-def _empty(shape, dtype, device, stream):
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _on(device, stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _operand(t, name, dtype=None):
+    """A contiguous CUDA tensor, of `dtype` if one is given; returns its device's index."""
+    try:
+        if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+            return t.get_device()
+    except AttributeError:
+        pass
+    _need_cuda(t, name, dtype)
+    return t.get_device()
 
 
 def _matrix(t, name, dtype=None):
-    _need_cuda(t, name, dtype)
+    """The same of a tensor with two dimensions."""
+    try:
+        if t.is_cuda and t.dim() == 2 and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+            return t.get_device()
+    except AttributeError:
+        pass
+    dev = _operand(t, name, dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    return dev
 
 
-def _codes(codes, scale, rows_per_scale, name):
-    """Checks a matrix of codes and its scales; returns its shape."""
+def _call(name, dev, stream, *args):
+    """lib().name(*args, stream) with device number `dev` current."""
     import torch
-    _matrix(codes, f"{name}_codes", torch.float8_e4m3fn)
-    _matrix(scale, f"{name}_scale", torch.float8_e8m0fnu)
-    n, d = codes.shape
-    check_fp8_width(d, f"the width of {name}_codes")
-    _need_shape(scale, (n if rows_per_scale == 1 else fp8_blocks(n), fp8_blocks(d)), f"{name}_scale")
-    return n, d
+    fn = getattr(lib(), name)
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with _on(torch.device("cuda", dev), stream):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check(rc, name)
 
 
-def _out(t, shape, dtype, device, stream, name):
+def _out(t, shape, dtype, like, stream, name, torch):
+    """The caller's matrix `t` after its checks, or a new one on the device of `like`."""
     if t is None:
-        return _empty(shape, dtype, device, stream)
-    _need_cuda(t, name, dtype)
-    _need_shape(t, shape, name)
+        if stream is None:
+            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+        with _on(like.device, stream):
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    if _operand(t, name, dtype) != like.get_device():
+        check_same_device(t, like)
+    if t.shape != shape:
+        _need_shape(t, shape, name)
     return t
+
+
+def _codes(codes, scale, rows_per_scale, names, torch):
+    """Checks a matrix of codes and its scales (`names`: what the caller calls
+    them); returns its device's index and its shape."""
+    dev = _matrix(codes, names[0], torch.float8_e4m3fn)
+    if _matrix(scale, names[1], torch.float8_e8m0fnu) != dev:
+        check_same_device(codes, scale)
+    n, d = codes.shape
+    if d <= 0 or d % 16:
+        check_fp8_width(d, f"the width of {names[0]}")
+    want = (n if rows_per_scale == 1 else -(-n // BLOCK), -(-d // BLOCK))
+    if scale.shape != want:
+        _need_shape(scale, want, names[1])
+    return dev, n, d
+
+
+_A, _W, _X = ("a_codes", "a_scale"), ("w_codes", "w_scale"), ("x_codes", "x_scale")
 
 
 def quantize_fp8(X, activation=None, checkpoint=False, codes=None, scale=None, stream=None):
@@ -89,7 +119,7 @@ def quantize_fp8(X, activation=None, checkpoint=False, codes=None, scale=None, s
     itself, from which gelu_backward_fp8 takes the gradient: (codes, scale,
     x_codes, x_scale).  d a multiple of 16."""
     import torch
-    _matrix(X, "X")
+    dev = _matrix(X, "X")
     dtype = _dtype_code(X)
     if activation not in _ACTS:
         raise ValueError("activation must be None, 'none' or 'gelu'")
@@ -98,16 +128,17 @@ def quantize_fp8(X, activation=None, checkpoint=False, codes=None, scale=None, s
         raise ValueError("checkpoint goes with an activation: without one the codes are X's own")
     T, d = X.shape
     check_fp8_width(d, "the width of X")
-    dev = X.device
-    codes = _out(codes, (T, d), torch.float8_e4m3fn, dev, stream, "codes")
-    scale = _out(scale, (T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream, "scale")
-    check_same_device(X, codes, scale)
+    blocks = (T, -(-d // BLOCK))
+    codes = _out(codes, (T, d), torch.float8_e4m3fn, X, stream, "codes", torch)
+    scale = _out(scale, blocks, torch.float8_e8m0fnu, X, stream, "scale", torch)
     if not checkpoint:
-        _call("quantize_fp8", dev, stream, X, dtype, T, d, act, codes, scale, None, None)
+        _call("quantize_fp8", dev, stream, X.data_ptr(), dtype, T, d, act, codes.data_ptr(), scale.data_ptr(), None,
+              None)
         return codes, scale
-    x_codes = _empty((T, d), torch.float8_e4m3fn, dev, stream)
-    x_scale = _empty((T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream)
-    _call("quantize_fp8", dev, stream, X, dtype, T, d, act, codes, scale, x_codes, x_scale)
+    x_codes = _out(None, (T, d), torch.float8_e4m3fn, X, stream, "x_codes", torch)
+    x_scale = _out(None, blocks, torch.float8_e8m0fnu, X, stream, "x_scale", torch)
+    _call("quantize_fp8", dev, stream, X.data_ptr(), dtype, T, d, act, codes.data_ptr(), scale.data_ptr(),
+          x_codes.data_ptr(), x_scale.data_ptr())
     return codes, scale, x_codes, x_scale
 
 
@@ -119,23 +150,22 @@ def quantize_weights_fp8(W, transposed=False, codes=None, scale=None, stream=Non
     the layer's input gradient: (codes, scale, codes_t [K, N], scale_t).
     K a multiple of 16, and N too when transposed."""
     import torch
-    _matrix(W, "W")
+    dev = _matrix(W, "W")
     dtype = _dtype_code(W)
     N, K = W.shape
     check_fp8_width(K, "the width of W")
     if transposed and N:
         check_fp8_width(N, "the height of W (the width of its transpose)")
-    dev = W.device
-    codes = _out(codes, (N, K), torch.float8_e4m3fn, dev, stream, "codes")
-    scale = _out(scale, (fp8_blocks(N), fp8_blocks(K)), torch.float8_e8m0fnu, dev, stream, "scale")
-    check_same_device(W, codes, scale)
+    codes = _out(codes, (N, K), torch.float8_e4m3fn, W, stream, "codes", torch)
+    scale = _out(scale, (fp8_blocks(N), fp8_blocks(K)), torch.float8_e8m0fnu, W, stream, "scale", torch)
     if not transposed:
-        _call("quantize_weights_fp8", dev, stream, W, dtype, N, K, codes, scale, None, None)
+        _call("quantize_weights_fp8", dev, stream, W.data_ptr(), dtype, N, K, codes.data_ptr(), scale.data_ptr(), None,
+              None)
         return codes, scale
-    codes_t = _empty((K, N), torch.float8_e4m3fn, dev, stream)
-    scale_t = _empty((fp8_blocks(K), fp8_blocks(N)), torch.float8_e8m0fnu, dev, stream)
-    _call("quantize_weights_fp8", dev, stream, W, dtype, N, K, codes, scale, codes_t if N else None,
-          scale_t if N else None)
+    codes_t = _out(None, (K, N), torch.float8_e4m3fn, W, stream, "codes_t", torch)
+    scale_t = _out(None, (fp8_blocks(K), fp8_blocks(N)), torch.float8_e8m0fnu, W, stream, "scale_t", torch)
+    _call("quantize_weights_fp8", dev, stream, W.data_ptr(), dtype, N, K, codes.data_ptr(), scale.data_ptr(),
+          codes_t.data_ptr() if N else None, scale_t.data_ptr() if N else None)
     return codes, scale, codes_t, scale_t
 
 
@@ -143,13 +173,15 @@ def qlinear_fp8(a_codes, a_scale, w_codes, w_scale, out=None, stream=None):
     """y[m, n] = sum_k (sa[m, k/128] qa[m, k]) (sw[n/128, k/128] qw[n, k]) as
     bfloat16 [M, N], on the codes of quantize_fp8 and quantize_weights_fp8."""
     import torch
-    M, K = _codes(a_codes, a_scale, 1, "a")
-    N, K2 = _codes(w_codes, w_scale, BLOCK, "w")
+    dev, M, K = _codes(a_codes, a_scale, 1, _A, torch)
+    dev_w, N, K2 = _codes(w_codes, w_scale, BLOCK, _W, torch)
     if K != K2:
         raise ValueError("a_codes and w_codes disagree on K")
-    dev = check_same_device(a_codes, a_scale, w_codes, w_scale, out)
-    out = _out(out, (M, N), torch.bfloat16, dev, stream, "out")
-    _call("qlinear_fp8", dev, stream, a_codes, a_scale, w_codes, w_scale, M, N, K, out)
+    if dev != dev_w:
+        check_same_device(a_codes, w_codes)
+    out = _out(out, (M, N), torch.bfloat16, a_codes, stream, "out", torch)
+    _call("qlinear_fp8", dev, stream, a_codes.data_ptr(), a_scale.data_ptr(), w_codes.data_ptr(), w_scale.data_ptr(),
+          M, N, K, out.data_ptr())
     return out
 
 
@@ -158,19 +190,21 @@ def qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype=None, out=None, stream=None):
     of qlinear_fp8 from the bfloat16 dY [M, N] and the codes kept of the
     layer's input; bfloat16 (the default) or float32 [N, K].  N a multiple of 8."""
     import torch
-    _matrix(dY, "dY", torch.bfloat16)
-    M, K = _codes(a_codes, a_scale, 1, "a")
-    N = dY.shape[1]
-    if dY.shape[0] != M:
+    dev_y = _matrix(dY, "dY", torch.bfloat16)
+    dev, M, K = _codes(a_codes, a_scale, 1, _A, torch)
+    T, N = dY.shape
+    if T != M:
         raise ValueError("dY and a_codes disagree on the number of tokens")
     if N:
         check_fp8_width(N, "the width of dY", 8)
     dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("the weight gradient is bfloat16 or float32")
-    dev = check_same_device(dY, a_codes, a_scale, out)
-    out = _out(out, (N, K), dtype, dev, stream, "out")
-    _call("qlinear_fp8_wgrad", dev, stream, dY, a_codes, a_scale, M, N, K, out, _dtype_code(out))
+    if dev != dev_y:
+        check_same_device(dY, a_codes)
+    out = _out(out, (N, K), dtype, dY, stream, "out", torch)
+    _call("qlinear_fp8_wgrad", dev, stream, dY.data_ptr(), a_codes.data_ptr(), a_scale.data_ptr(), M, N, K,
+          out.data_ptr(), RBQ_BF16 if dtype is torch.bfloat16 else RBQ_F32)
     return out
 
 
@@ -182,17 +216,21 @@ def gelu_backward_fp8(dH, x_codes, x_scale, quantize=False, out=None, stream=Non
     quantize=True also returns quantize_fp8(dX), for the product that follows:
     (dX, codes, scale)."""
     import torch
-    _matrix(dH, "dH", torch.bfloat16)
-    T, d = _codes(x_codes, x_scale, 1, "x")
-    _need_shape(dH, (T, d), "dH")
-    dev = check_same_device(dH, x_codes, x_scale, out)
-    out = _out(out, (T, d), torch.bfloat16, dev, stream, "out")
+    dev_h = _matrix(dH, "dH", torch.bfloat16)
+    dev, T, d = _codes(x_codes, x_scale, 1, _X, torch)
+    if dH.shape != (T, d):
+        _need_shape(dH, (T, d), "dH")
+    if dev != dev_h:
+        check_same_device(dH, x_codes)
+    out = _out(out, (T, d), torch.bfloat16, dH, stream, "out", torch)
     if not quantize:
-        _call("gelu_backward_fp8", dev, stream, dH, x_codes, x_scale, T, d, out, None, None)
+        _call("gelu_backward_fp8", dev, stream, dH.data_ptr(), x_codes.data_ptr(), x_scale.data_ptr(), T, d,
+              out.data_ptr(), None, None)
         return out
-    codes = _empty((T, d), torch.float8_e4m3fn, dev, stream)
-    scale = _empty((T, fp8_blocks(d)), torch.float8_e8m0fnu, dev, stream)
-    _call("gelu_backward_fp8", dev, stream, dH, x_codes, x_scale, T, d, out, codes, scale)
+    codes = _out(None, (T, d), torch.float8_e4m3fn, dH, stream, "codes", torch)
+    scale = _out(None, x_scale.shape, torch.float8_e8m0fnu, dH, stream, "scale", torch)
+    _call("gelu_backward_fp8", dev, stream, dH.data_ptr(), x_codes.data_ptr(), x_scale.data_ptr(), T, d,
+          out.data_ptr(), codes.data_ptr(), scale.data_ptr())
     return out, codes, scale
 
 
