@@ -10,12 +10,18 @@
 
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "rbq_fp8.cuh"
 #include "rbq_internal.h"
+#include "rbq_sm100.cuh"
 
 namespace rbq {
 namespace fp8 {
 namespace {
+
+using sm100::griddep_launch_dependents;
+using sm100::griddep_wait;
 
 // A thread holds 16 consecutive values of a row (d is a multiple of 16); the
 // 8 threads of a block of 128 find its maximum by shuffles.
@@ -23,37 +29,138 @@ constexpr int kVals = 16;
 constexpr int kLanesPerBlock = kBlock / kVals;
 constexpr int kThreads = 256;
 constexpr int kBlocksPerCta = kThreads / kLanesPerBlock;
+constexpr uint32_t kNaN = 0x7FFFFFFFu;
 
-// Eight / sixteen values of `src` (16-byte aligned) as fp32.
-__device__ __forceinline__ void load16(const uint16_t* src, float (&x)[kVals]) {
+// ---- pairs of fp32 in one 64-bit register, for the packed FMA ------------------
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 both(float v) { return pack(v, v); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---- loads and stores -----------------------------------------------------------
+// 32 bytes in one instruction where the address allows it (`wide`), two of 16 elsewhere.
+__device__ __forceinline__ void load32(const void* src, bool wide, uint32_t* w) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(src));
+  } else {
+    const uint4 a = static_cast<const uint4*>(src)[0], b = static_cast<const uint4*>(src)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* dst, bool wide, const uint32_t* w) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Sixteen values of a row as they are stored: 8 words of two BF16, or 16 of one fp32.
+template <typename T>
+struct Piece {
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr int kWords = kF32 ? 16 : 8;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint4 v = reinterpret_cast<const uint4*>(src)[j];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* src, bool wide) {
+    load32(src, wide, w);
+    if constexpr (kF32) load32(src + 8, wide, w + 8);
+  }
+  __device__ __forceinline__ f2 pair(int i) const {
+    if constexpr (kF32)
+      return pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else
+      return pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  // Largest magnitude; NaN is passed over.
+  __device__ __forceinline__ float amax() const {
+    if constexpr (kF32) {
+      float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
-      x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      for (int i = 0; i < 16; i += 2)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i])), fabsf(__uint_as_float(w[i + 1]))));
+      return m;
+    } else {
+      __nv_bfloat162 m = __habs2(half_pair(0));
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(half_pair(i)));
+      return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
     }
   }
-}
-__device__ __forceinline__ void load16(const float* src, float (&x)[kVals]) {
+  __device__ __forceinline__ void drop_infinities() {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 v = reinterpret_cast<const float4*>(src)[j];
-    x[4 * j] = v.x;
-    x[4 * j + 1] = v.y;
-    x[4 * j + 2] = v.z;
-    x[4 * j + 3] = v.w;
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (kF32) {
+        if ((w[i] & 0x7FFFFFFFu) == 0x7F800000u) w[i] = kNaN;
+      } else {
+        if ((w[i] & 0x7FFFu) == 0x7F80u) w[i] |= 0x7Fu;
+        if ((w[i] & 0x7FFF0000u) == 0x7F800000u) w[i] |= 0x7F0000u;
+      }
+    }
   }
-}
 
-__device__ __forceinline__ float amax16(const float (&x)[kVals]) {
-  float m = fabsf(x[0]);
+ private:
+  __device__ __forceinline__ __nv_bfloat162 half_pair(int i) const {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+  }
+};
+// Sixteen values as pairs of fp32.
+struct Pairs {
+  f2 v[kVals / 2];
+  __device__ __forceinline__ f2 pair(int i) const { return v[i]; }
+  __device__ __forceinline__ float amax() const {
+    float m = 0.f;
 #pragma unroll
-  for (int i = 1; i < kVals; ++i) m = fmaxf(m, fabsf(x[i]));     // NaN is passed over
-  return m;
-}
+    for (int i = 0; i < kVals / 2; ++i) {
+      float a, b;
+      unpack(v[i], a, b);
+      m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+    }
+    return m;
+  }
+  __device__ __forceinline__ void drop_infinities() {
+#pragma unroll
+    for (int i = 0; i < kVals / 2; ++i) {
+      float a, b;
+      unpack(v[i], a, b);
+      if (fabsf(a) == INFINITY) a = __uint_as_float(kNaN);
+      if (fabsf(b) == INFINITY) b = __uint_as_float(kNaN);
+      v[i] = pack(a, b);
+    }
+  }
+};
+
 // Maximum over the 8 threads of a block (every lane of the warp takes part).
 __device__ __forceinline__ float block_max(float m) {
 #pragma unroll
@@ -64,167 +171,201 @@ __device__ __forceinline__ float block_max(float m) {
 // The scale byte of the block this thread's 16 values belong to.  An infinity
 // has no E4M3 value: it becomes NaN (and so reaches the result) and does not
 // count for the maximum, which would otherwise flush its 127 neighbours.
-__device__ __forceinline__ uint32_t block_scale(float (&x)[kVals]) {
-  float m = block_max(amax16(x));
+template <typename V>
+__device__ __forceinline__ uint32_t block_scale(V& x) {
+  float m = block_max(x.amax());
   if (__any_sync(0xffffffffu, m == INFINITY)) {
-#pragma unroll
-    for (int i = 0; i < kVals; ++i)
-      if (fabsf(x[i]) == INFINITY) x[i] = __uint_as_float(0x7FFFFFFFu);
-    m = block_max(amax16(x));
-    if (!(m >= 0.f)) m = 0.f;                                     // nothing but NaN
+    x.drop_infinities();
+    m = block_max(x.amax());
   }
-  return scale_byte(m >= 0.f ? m : 0.f);
+  return scale_byte(m);
 }
 
-__device__ __forceinline__ uint4 encode16(const float (&x)[kVals], float inv) {
+template <typename V>
+__device__ __forceinline__ uint4 encode16(const V& x, float inv) {
+  const f2 k = both(inv);
   uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = encode4(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
+  for (int j = 0; j < 4; ++j) {
+    float a, b, c, d;
+    unpack(mul2(x.pair(2 * j), k), a, b);
+    unpack(mul2(x.pair(2 * j + 1), k), c, d);
+    w[j] = encode4(a, b, c, d);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Phi(x) and exp(-x^2 / 2): the normal CDF from Abramowitz & Stegun (1964),
-// formula 7.1.26 (Hastings' approximation of erf, |error| <= 1.5e-7), which
-// shares its exponential with the density.
-__device__ __forceinline__ void normal_cdf(float x, float& cdf, float& e) {
-  const float z = fabsf(x) * 0.70710678118654752f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  e = __expf(-z * z);
-  const float tail = 0.5f * t * p * e;
-  cdf = x >= 0.f ? 1.0f - tail : tail;
+// ---- the GELU --------------------------------------------------------------------
+// Phi(-z) = 2^Q(z), z = |x|: Q is a polynomial of degree 8, fitted here to
+// log2 Phi(-z) on [0, 7] by iteratively reweighted least squares so that the
+// largest of |error| / max(Phi(-z), 1e-5) is least.  Evaluated in fp32,
+// |error of Phi| <= 8e-8 everywhere, and 9e-4 of Phi(-z) itself to z = 5, 4e-3
+// to z = 7 (an E4M3 code's half step is 6e-2); beyond, it falls below 2e-12 and
+// on to 0.  One exponential and no reciprocal: with erf's usual rational
+// approximation the kernel was bound by its instructions (38 a value).
+//
+// Everything works on n = -|x| (so the odd coefficients' signs are turned),
+// two values to an instruction.
+__device__ __forceinline__ f2 normal_tail(f2 n) {
+  f2 q = fma2(both(-8.438778991e-07f), n, both(-1.533665090e-05f));
+  q = fma2(q, n, both(-7.393999113e-05f));
+  q = fma2(q, n, both(3.969362006e-04f));
+  q = fma2(q, n, both(7.381424308e-03f));
+  q = fma2(q, n, both(5.269747227e-02f));
+  q = fma2(q, n, both(-4.591485262e-01f));
+  q = fma2(q, n, both(1.151111722e+00f));
+  q = fma2(q, n, both(-9.999998808e-01f));
+  float a, b;
+  unpack(q, a, b);
+  return pack(ex2(a), ex2(b));
 }
-__device__ __forceinline__ float gelu(float x) {
-  float cdf, e;
-  normal_cdf(x, cdf, e);
-  return x * cdf;
+__device__ __forceinline__ float minus_abs(float x) { return __uint_as_float(__float_as_uint(x) | 0x80000000u); }
+// x Phi(x) = max(x, 0) - |x| Phi(-|x|)
+__device__ __forceinline__ f2 gelu(f2 x) {
+  float a, b;
+  unpack(x, a, b);
+  const f2 n = pack(minus_abs(a), minus_abs(b));
+  return fma2(n, normal_tail(n), pack(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-// d/dx x Phi(x) = Phi(x) + x phi(x), phi(x) = exp(-x^2 / 2) / sqrt(2 pi).
-__device__ __forceinline__ float gelu_slope(float x) {
-  float cdf, e;
-  normal_cdf(x, cdf, e);
-  return fmaf(x * 0.39894228040143268f, e, cdf);
+// d/dx x Phi(x) = Phi(x) + x phi(x), phi(x) = exp(-x^2 / 2) / sqrt(2 pi):
+// g = Phi(-|x|) - |x| phi(x) for x < 0, 1 - g for x >= 0.
+__device__ __forceinline__ f2 gelu_slope(f2 x) {
+  float a, b;
+  unpack(x, a, b);
+  const f2 n = pack(minus_abs(a), minus_abs(b));
+  // log2 phi = -x^2 log2(e) / 2 - log2(2 pi) / 2
+  float u, v;
+  unpack(fma2(mul2(x, both(-0.72134752044f)), x, both(-1.32574806473f)), u, v);
+  const f2 g = fma2(n, pack(ex2(u), ex2(v)), normal_tail(n));
+  float g0, g1, h0, h1;
+  unpack(g, g0, g1);
+  unpack(fma2(g, both(-1.0f), both(1.0f)), h0, h1);
+  return pack(a >= 0.f ? h0 : g0, b >= 0.f ? h1 : g1);
 }
 
-// Where a group of 8 threads works: row, block of the row, this thread's
-// first column.
-struct Place {
-  long long row;
-  int kb, col;
-  bool in;
+// ---- where a group of 8 threads works ---------------------------------------------
+struct Rows {
+  long long total;        // blocks of 128 in all
+  int d, kbs;
+  uint32_t mul;           // b / kbs = (b mul) >> shift for b < 2^31
+  int shift;
+  int wide;               // 32-byte accesses to the 16-bit (or fp32) rows
 };
-__device__ __forceinline__ Place place(long long total, int d, int kbs) {
+struct Place {
+  long long off, so;      // this thread's first value, the block's scale
+  bool in, lead;
+};
+__device__ __forceinline__ Place place(const Rows& r) {
   const long long b = static_cast<long long>(blockIdx.x) * kBlocksPerCta + threadIdx.x / kLanesPerBlock;
+  const long long row = r.total <= 0x7FFFFFFFll - kBlocksPerCta
+                            ? static_cast<long long>((static_cast<unsigned long long>(b) * r.mul) >> r.shift)
+                            : b / r.kbs;
+  const int sub = threadIdx.x % kLanesPerBlock;
+  const int col = static_cast<int>(b - row * r.kbs) * kBlock + sub * kVals;
   Place p;
-  p.row = b <= 0xFFFFFFFFll ? static_cast<uint32_t>(b) / static_cast<uint32_t>(kbs) : b / kbs;
-  p.kb = static_cast<int>(b - p.row * kbs);
-  p.col = p.kb * kBlock + (threadIdx.x % kLanesPerBlock) * kVals;
-  p.in = b < total && p.col < d;                    // the last block of a row may be short
+  p.in = b < r.total && col < r.d;                    // the last block of a row may be short
+  p.lead = sub == 0 && p.in;
+  p.off = row * r.d + col;
+  p.so = b;
   return p;
 }
 
 template <typename T, bool GELU, bool CKPT>
-__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const T* X, long long total, int d, int kbs,
-                                                                uint8_t* codes, uint8_t* scales, uint8_t* xcodes,
-                                                                uint8_t* xscales) {
-  const Place p = place(total, d, kbs);
-  const long long off = p.row * d + p.col, so = p.row * kbs + p.kb;
-  const bool lead = threadIdx.x % kLanesPerBlock == 0 && p.in;
-  float x[kVals] = {};
-  if (p.in) load16(X + off, x);
-  if constexpr (CKPT) {
-    float y[kVals];
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) y[i] = x[i];
-    const uint32_t s = block_scale(y);
-    if (p.in) *reinterpret_cast<uint4*>(xcodes + off) = encode16(y, inv_scale(s));
-    if (lead) xscales[so] = static_cast<uint8_t>(s);
-  }
+__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const T* X, const Rows r, uint8_t* codes,
+                                                                uint8_t* scales, uint8_t* xcodes, uint8_t* xscales) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Place p = place(r);
+  Piece<T> x;
+  x.zero();
+  if (p.in) x.load(X + p.off, r.wide);
+  Pairs h;
   if constexpr (GELU) {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) x[i] = gelu(x[i]);
+    for (int i = 0; i < kVals / 2; ++i) h.v[i] = gelu(x.pair(i));
   }
-  const uint32_t s = block_scale(x);
-  if (p.in) *reinterpret_cast<uint4*>(codes + off) = encode16(x, inv_scale(s));
-  if (lead) scales[so] = static_cast<uint8_t>(s);
+  if constexpr (CKPT || !GELU) {
+    const uint32_t s = block_scale(x);
+    if (p.in) *reinterpret_cast<uint4*>((GELU ? xcodes : codes) + p.off) = encode16(x, inv_scale(s));
+    if (p.lead) (GELU ? xscales : scales)[p.so] = static_cast<uint8_t>(s);
+  }
+  if constexpr (GELU) {
+    const uint32_t s = block_scale(h);
+    if (p.in) *reinterpret_cast<uint4*>(codes + p.off) = encode16(h, inv_scale(s));
+    if (p.lead) scales[p.so] = static_cast<uint8_t>(s);
+  }
 }
 
 template <bool QUANT>
 __global__ void __launch_bounds__(kThreads) gelu_backward_fp8_kernel(const uint16_t* dH, const uint8_t* xcodes,
-                                                                     const uint8_t* xscales, long long total, int d,
-                                                                     int kbs, uint16_t* dX, uint8_t* codes,
-                                                                     uint8_t* scales) {
-  const Place p = place(total, d, kbs);
-  const long long off = p.row * d + p.col, so = p.row * kbs + p.kb;
-  float g[kVals] = {};
+                                                                     const uint8_t* xscales, const Rows r,
+                                                                     uint16_t* dX, uint8_t* codes, uint8_t* scales) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Place p = place(r);
+  Piece<uint16_t> g;
+  g.zero();
   if (p.in) {
-    load16(dH + off, g);
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(xcodes + off));
-    const float s = scale_value(xscales[so]);
+    g.load(dH + p.off, r.wide);
+    const uint4 c = *reinterpret_cast<const uint4*>(xcodes + p.off);
+    const f2 s = both(scale_value(xscales[p.so]));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[kVals / 2];
 #pragma unroll
     for (int i = 0; i < kVals / 2; ++i) {
       const float2 v = decode2(w[i / 2] >> (16 * (i & 1)));
-      const __nv_bfloat162 r = __floats2bfloat162_rn(g[2 * i] * gelu_slope(v.x * s), g[2 * i + 1] * gelu_slope(v.y * s));
-      o[i] = *reinterpret_cast<const uint32_t*>(&r);
-      g[2 * i] = __uint_as_float(o[i] << 16);              // the codes are those of the BF16 gradient
-      g[2 * i + 1] = __uint_as_float(o[i] & 0xFFFF0000u);
+      float a, b;
+      unpack(mul2(g.pair(i), gelu_slope(mul2(pack(v.x, v.y), s))), a, b);
+      const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
+      g.w[i] = *reinterpret_cast<const uint32_t*>(&o);      // the codes are those of the BF16 gradient
     }
-    uint4* dst = reinterpret_cast<uint4*>(dX + off);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    store32(dX + p.off, r.wide, g.w);
   }
   if constexpr (QUANT) {
     const uint32_t s = block_scale(g);
-    if (p.in) {
-      *reinterpret_cast<uint4*>(codes + off) = encode16(g, inv_scale(s));
-      if (threadIdx.x % kLanesPerBlock == 0) scales[so] = static_cast<uint8_t>(s);
-    }
+    if (p.in) *reinterpret_cast<uint4*>(codes + p.off) = encode16(g, inv_scale(s));
+    if (p.lead) scales[p.so] = static_cast<uint8_t>(s);
   }
 }
 
 // One CTA per 128 x 128 block: thread (row t / 8 + 32 i, columns 16 (t % 8))
-// holds 4 x 16 values.  The transposed codes go through shared memory: row n's
-// 16-byte piece c is kept at piece c ^ (n / 16), so that both the 16-byte
-// writes (a row per 8 lanes) and the word reads of the transposition (8 row
-// groups x 4 words per warp) touch all 32 banks once.
+// holds 4 x 16 values as they were loaded.  The transposed codes go through
+// shared memory: row n's 16-byte piece c is kept at piece c ^ (n / 16), so that
+// both the 16-byte writes (a row per 8 lanes) and the word reads of the
+// transposition (8 row groups x 4 words per warp) touch all 32 banks once.
 template <typename T, bool TRANS>
-__global__ void __launch_bounds__(kThreads) quantize_weights_fp8_kernel(const T* W, int N, int K, int nbs, int kbs,
-                                                                        uint8_t* codes, uint8_t* scales,
-                                                                        uint8_t* codes_t, uint8_t* scales_t) {
-  __shared__ float wmax[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+    quantize_weights_fp8_kernel(const T* W, int N, int K, int nbs, int kbs, int wide, uint8_t* codes, uint8_t* scales,
+                                uint8_t* codes_t, uint8_t* scales_t) {
+  __shared__ float wmax[2][kThreads / 32];
   __shared__ __align__(16) uint32_t tile[TRANS ? kBlock * kBlock / 4 : 4];
+  griddep_wait();
+  griddep_launch_dependents();
   const int kb = blockIdx.x % kbs, nb = blockIdx.x / kbs;
   const int sub = threadIdx.x % kLanesPerBlock, r0 = threadIdx.x / kLanesPerBlock;
   const int col = kb * kBlock + sub * kVals;
-  float x[4][kVals];
-  float m = 0.f;
+  Piece<T> x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = nb * kBlock + r0 + 32 * i;
-#pragma unroll
-    for (int j = 0; j < kVals; ++j) x[i][j] = 0.f;
-    if (row < N && col < K) load16(W + static_cast<long long>(row) * K + col, x[i]);
+    x[i].zero();
+    if (row < N && col < K) x[i].load(W + static_cast<long long>(row) * K + col, wide);
   }
+  float m = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, x[i].amax());
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      if (fabsf(x[i][j]) == INFINITY) x[i][j] = __uint_as_float(0x7FFFFFFFu);   // as block_scale
-      m = fmaxf(m, fabsf(x[i][j]));
-    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) wmax[pass][threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[pass][i]);
+    if (m != INFINITY) break;                                    // the same in every thread
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i].drop_infinities();          // as block_scale
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
   const uint32_t s = scale_byte(m);
   const float inv = inv_scale(s);
   if (threadIdx.x == 0) {
@@ -265,11 +406,39 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_fp8_kernel(const T*
   }
 }
 
-int launched() {
-  const cudaError_t e = cudaGetLastError();
+// The next kernel of the stream may set itself up while this one runs (each
+// waits for the one before it to end before it touches memory).
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), unsigned grid, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
 }
 
+Rows make_rows(int T, int d, bool wide) {
+  Rows r{};
+  r.d = d;
+  r.kbs = blocks(d);
+  r.total = static_cast<long long>(T) * r.kbs;
+  // With 2^s >= kbs and mul = ceil(2^(31 + s) / kbs), mul kbs = 2^(31 + s) + e,
+  // e < kbs <= 2^s, so for b < 2^31 the quotient's error b e / (kbs 2^(31 + s)) is
+  // below 1 / kbs: the shift gives floor(b / kbs).
+  int s = 0;
+  while ((1ll << s) < r.kbs) ++s;
+  r.mul = static_cast<uint32_t>(((1ull << (31 + s)) + r.kbs - 1) / r.kbs);
+  r.shift = 31 + s;
+  r.wide = wide;
+  return r;
+}
 // CTAs for `total` blocks, 0 when the grid cannot hold them.
 unsigned grid_of(long long total) {
   const long long g = (total + kBlocksPerCta - 1) / kBlocksPerCta;
@@ -277,19 +446,14 @@ unsigned grid_of(long long total) {
 }
 
 template <typename T>
-int launch_quantize(const void* X, long long total, int d, bool gelu, uint8_t* codes, uint8_t* scales,
-                    uint8_t* xcodes, uint8_t* xscales, cudaStream_t st) {
-  const unsigned grid = grid_of(total);
+int launch_quantize(const void* X, const Rows& r, bool gelu, uint8_t* codes, uint8_t* scales, uint8_t* xcodes,
+                    uint8_t* xscales, cudaStream_t st) {
+  const unsigned grid = grid_of(r.total);
   if (!grid) return RBQ_EINVAL;
   const T* x = static_cast<const T*>(X);
-  const int kbs = blocks(d);
-  if (gelu && xcodes)
-    quantize_fp8_kernel<T, true, true><<<grid, kThreads, 0, st>>>(x, total, d, kbs, codes, scales, xcodes, xscales);
-  else if (gelu)
-    quantize_fp8_kernel<T, true, false><<<grid, kThreads, 0, st>>>(x, total, d, kbs, codes, scales, nullptr, nullptr);
-  else
-    quantize_fp8_kernel<T, false, false><<<grid, kThreads, 0, st>>>(x, total, d, kbs, codes, scales, nullptr, nullptr);
-  return launched();
+  if (gelu && xcodes) return launch(quantize_fp8_kernel<T, true, true>, grid, st, x, r, codes, scales, xcodes, xscales);
+  if (gelu) return launch(quantize_fp8_kernel<T, true, false>, grid, st, x, r, codes, scales, xcodes, xscales);
+  return launch(quantize_fp8_kernel<T, false, false>, grid, st, x, r, codes, scales, xcodes, xscales);
 }
 
 template <typename T>
@@ -300,11 +464,12 @@ int launch_weights(const void* W, int N, int K, uint8_t* codes, uint8_t* scales,
   if (grid > 0x7FFFFFFFll) return RBQ_EINVAL;
   const T* w = static_cast<const T*>(W);
   const unsigned g = static_cast<unsigned>(grid);
+  const int wide = aligned(W, 32);                 // rows are multiples of 32 bytes
   if (codes_t)
-    quantize_weights_fp8_kernel<T, true><<<g, kThreads, 0, st>>>(w, N, K, nbs, kbs, codes, scales, codes_t, scales_t);
-  else
-    quantize_weights_fp8_kernel<T, false><<<g, kThreads, 0, st>>>(w, N, K, nbs, kbs, codes, scales, nullptr, nullptr);
-  return launched();
+    return launch(quantize_weights_fp8_kernel<T, true>, g, st, w, N, K, nbs, kbs, wide, codes, scales, codes_t,
+                  scales_t);
+  return launch(quantize_weights_fp8_kernel<T, false>, g, st, w, N, K, nbs, kbs, wide, codes, scales, codes_t,
+                scales_t);
 }
 
 }  // namespace
@@ -321,12 +486,12 @@ extern "C" int quantize_fp8(const void* X, int dtype, int T, int d, int activati
   if (T == 0) return RBQ_OK;
   if (!X || !codes || !scales) return RBQ_EINVAL;
   if (!aligned(X, 16) || !aligned(codes, 16) || (x_codes && !aligned(x_codes, 16))) return RBQ_EALIGN;
-  const long long total = static_cast<long long>(T) * fp8::blocks(d);
+  const fp8::Rows r = fp8::make_rows(T, d, aligned(X, 32));          // rows are multiples of 32 bytes
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool gelu = activation == RBQ_ACT_GELU;
   return dtype == RBQ_BF16
-             ? fp8::launch_quantize<uint16_t>(X, total, d, gelu, codes, scales, x_codes, x_scales, st)
-             : fp8::launch_quantize<float>(X, total, d, gelu, codes, scales, x_codes, x_scales, st);
+             ? fp8::launch_quantize<uint16_t>(X, r, gelu, codes, scales, x_codes, x_scales, st)
+             : fp8::launch_quantize<float>(X, r, gelu, codes, scales, x_codes, x_scales, st);
 }
 
 extern "C" int quantize_weights_fp8(const void* W, int dtype, int N, int K, uint8_t* codes, uint8_t* scales,
@@ -348,16 +513,10 @@ extern "C" int gelu_backward_fp8(const uint16_t* dH, const uint8_t* x_codes, con
   if (!dH || !x_codes || !x_scales || !dX) return RBQ_EINVAL;
   if (!aligned(dH, 16) || !aligned(x_codes, 16) || !aligned(dX, 16) || (codes && !aligned(codes, 16)))
     return RBQ_EALIGN;
-  const long long total = static_cast<long long>(T) * fp8::blocks(d);
-  const unsigned grid = fp8::grid_of(total);
+  const fp8::Rows r = fp8::make_rows(T, d, aligned(dH, 32) && aligned(dX, 32));
+  const unsigned grid = fp8::grid_of(r.total);
   if (!grid) return RBQ_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int kbs = fp8::blocks(d);
-  if (codes)
-    fp8::gelu_backward_fp8_kernel<true>
-        <<<grid, fp8::kThreads, 0, st>>>(dH, x_codes, x_scales, total, d, kbs, dX, codes, scales);
-  else
-    fp8::gelu_backward_fp8_kernel<false>
-        <<<grid, fp8::kThreads, 0, st>>>(dH, x_codes, x_scales, total, d, kbs, dX, nullptr, nullptr);
-  return fp8::launched();
+  const auto kernel = codes ? fp8::gelu_backward_fp8_kernel<true> : fp8::gelu_backward_fp8_kernel<false>;
+  return fp8::launch(kernel, grid, st, dH, x_codes, x_scales, r, dX, codes, scales);
 }
