@@ -61,5 +61,22 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// True in one thread of a converged warp, the one that issues its MMAs or its
+// TMA copies.  The operands of both are uniform registers: under a test of the
+// lane number the compiler moves each of them there by a loop over the threads
+// that might be active (173 cycles a tcgen05.mma; a 256 x 256 x 32 one runs for 128), under
+// elect.sync it knows that there is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
+}
+// The warp's number, in a form that the compiler knows to be the same in all its threads.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
 }  // namespace fp8
 }  // namespace rbq

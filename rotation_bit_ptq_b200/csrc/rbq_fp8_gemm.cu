@@ -108,18 +108,101 @@ __device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
                : "memory");
 }
 
-// The scale bytes of K slices kb .. kb + 3 of one row of scales (kbs per row),
-// those past `end` as 0 (their codes are zero or not multiplied).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int end, bool vec) {
-  if (vec && kb + kGroup <= end) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
-  uint32_t w = 0;
+// The scale bytes of a row from some K slice on, a word of four slices after
+// the other, one load each.  ALIGNED: every row is whole words.  Otherwise a row may
+// start at any address, and each of its words is put together from two
+// aligned ones, the second of which serves the next word too.  (Byte by byte,
+// the 512 x 1536 x 8960 layer, whose rows have 70 scales, took 38 us in place of 31.)
+// Loaded words may hold bytes of the rows beside it, but never of anything outside the
+// matrix of scales [lo, hi); what follows the row's last slice is not multiplied.
+template <bool ALIGNED>
+struct ScaleRow {
+  // one group's word, not put together yet: whoever loads it does not wait for it
+  struct Word {
+    uint32_t word, first, shift;       // `first` counts in a row's first group only
+  };
+  const uint8_t *at, *lo, *hi;
+  uint32_t shift, first;
+  __device__ __forceinline__ void start(const uint8_t* row, const uint8_t* matrix, long long bytes) {
+    at = row;
+    if constexpr (!ALIGNED) {
+      const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
+      lo = matrix;
+      hi = matrix + bytes;
+      shift = 8u * o;
+      at = row - o;
+      first = load();
+    }
+  }
+  __device__ __forceinline__ void none() {
+    at = lo = hi = nullptr;
+    shift = first = 0u;
+  }
+  __device__ __forceinline__ Word next() {
+    if constexpr (ALIGNED) {
+      const uint32_t w = at ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
+      at = at ? at + kGroup : at;
+      return {w, 0u, 0u};
+    } else {
+      return {load(), first, shift};
+    }
+  }
+  // The group's scales; `carry`: the row's last word.
+  __device__ __forceinline__ static uint32_t join(const Word& w, bool first_group, uint32_t& carry) {
+    if constexpr (ALIGNED) {
+      return w.word;
+    } else {
+      const uint32_t s = __funnelshift_r(first_group ? w.first : carry, w.word, w.shift);
+      carry = w.word;
+      return s;
+    }
+  }
+
+ private:
+  __device__ __forceinline__ uint32_t load() {
+    const uint8_t* p = at;
+    at += kGroup;
+    if (p >= lo && p + kGroup <= hi) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j)
-    if (kb + j < end) w |= static_cast<uint32_t>(__ldg(row + kb + j)) << (8 * j);
-  return w;
-}
+    for (int j = 0; j < kGroup; ++j)
+      if (p + j >= lo && p + j < hi) w |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+    return w;
+  }
+};
 __device__ __forceinline__ void put_scale_word(uint8_t* block, int r, uint32_t w) {
   *reinterpret_cast<uint32_t*>(block + 16 * (r & 31) + 4 * (r >> 5)) = w;
+}
+
+enum Group { kNoGroup, kFirstGroup, kNextGroup };      // of a tile's row
+
+// One thread (row r) of the scale loaders: the words of group after group, W a
+// group, to the slots of the ring `sf`.  `fetch(w)` loads the next group's
+// words, `slot_free(slot, use)` waits until the MMAs are done with the slot's
+// last contents (false: gave up), `filled(slot)` reports.  The loads run
+// kSfSlots groups ahead, and nothing here looks at a word before its turn.
+template <int W, bool ALIGNED, typename Fetch, typename Free, typename Filled>
+__device__ __forceinline__ bool feed_scales(Fetch fetch, uint8_t* sf, int r, Free slot_free, Filled filled) {
+  typename ScaleRow<ALIGNED>::Word w[kSfSlots][W];
+  int have[kSfSlots];
+  uint32_t carry[W];
+#pragma unroll
+  for (int i = 0; i < kSfSlots; ++i) have[i] = fetch(w[i]);
+  for (uint32_t use = 0;; ++use) {
+#pragma unroll
+    for (int i = 0; i < kSfSlots; ++i) {
+      if (have[i] == kNoGroup) return true;
+      if (!slot_free(i, use)) return false;
+      uint8_t* block = sf + i * W * kSfBlock;
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        put_scale_word(block + j * kSfBlock, r, ScaleRow<ALIGNED>::join(w[i][j], have[i] == kFirstGroup, carry[j]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      filled(i);
+      have[i] = fetch(w[i]);
+    }
+  }
 }
 
 struct Params {
@@ -129,7 +212,8 @@ struct Params {
   uint16_t* Y;
   unsigned int* err;
   int order;                  // tile order (tiles::TileOrder)
-  int sf_vec;                 // scale rows readable as words (kbs % 4 == 0, aligned)
+  int sf_words;               // every part of a scale row that a CTA reads is whole words
+  int y_four;                 // rows of Y 8-byte aligned
   int y_vec;                  // 2: rows of Y 32-byte aligned, 1: 16-byte aligned, 0: neither
 };
 
@@ -158,7 +242,86 @@ struct __align__(8) Tail {
   volatile uint32_t abort;
 };
 
-constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + sizeof(Tail) + 64;
+constexpr int kTurn = 32 * 17;            // words a warp turns a 32 x 32 piece of the output in
+constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + 4 * 4 * kTurn + sizeof(Tail) + 64;
+
+// A warp's 32 rows x 32 columns of the output (row m0 + lane in each lane, 16
+// words of two BF16) to rows whose length or address allows no vectors (an odd
+// N, the right edge).  Through shared memory, rows of 17 words, so that 16 lanes write
+// one row with 4-byte stores: row by lane, each 2-byte store of the warp falls
+// into 32 sectors (a 333 x 1001 x 1552 layer took 44 us).  Where a row begins in
+// the middle of a word, its words are put together from two neighbours and
+// its two ends go out as halves.
+__device__ __forceinline__ void put_rows(uint32_t* turn, int lane, const uint32_t (&o)[16], const Params& p, int m0,
+                                         int nb) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) turn[17 * lane + j] = o[j];
+  __syncwarp();
+  const int l = lane & 15, cols = min(32, p.N - nb);
+  uint32_t w[16], next[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t* row = turn + 17 * (2 * i + (lane >> 4));
+    w[i] = row[l];
+    next[i] = row[min(l + 1, 15)];
+  }
+  uint16_t* dst = p.Y + static_cast<long long>(m0 + (lane >> 4)) * p.N + nb + 2 * l;
+  const int rows = p.M - m0 - (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < 16; ++i, dst += 2 * static_cast<long long>(p.N)) {
+    const int odd = (reinterpret_cast<uintptr_t>(dst) & 2u) != 0;      // the row begins in the middle of a word
+    const bool in = 2 * i < rows;
+    const bool whole = 2 * l + odd + 1 < cols;                         // never for l = 15 when odd
+    if (in && whole) *reinterpret_cast<uint32_t*>(dst + odd) = odd ? __byte_perm(w[i], next[i], 0x5432) : w[i];
+    if (in && !whole && 2 * l + odd < cols) dst[odd] = static_cast<uint16_t>(odd ? w[i] >> 16 : w[i]);
+    if (in && odd && l == 0) dst[0] = static_cast<uint16_t>(w[i]);
+  }
+  __syncwarp();
+}
+
+// The scale loaders of one CTA of a pair: its 128 rows of A, all 256 of B.
+template <bool ALIGNED>
+__device__ __forceinline__ bool load_pair_scales(const Params& p, Tail& tl, uint8_t* sf, uint32_t rank, int tile,
+                                                 int tstep) {
+  const int r = threadIdx.x - 32 * kScaleWarp, lane = threadIdx.x & 31;
+  const int ntiles_m = (p.M + 2 * kBM - 1) / (2 * kBM), ntiles_n = (p.N + kBN - 1) / kBN;
+  const int ntiles = ntiles_m * ntiles_n, last_nb = blocks(p.N) - 1;
+  const long long sa_bytes = static_cast<long long>(p.M) * p.kbs, sw_bytes = (last_nb + 1ll) * p.kbs;
+  int kb = 0;
+  ScaleRow<ALIGNED> ra, rb0, rb1;
+  // the words of the next group of K slices, of this tile or the next
+  const auto fetch = [&](typename ScaleRow<ALIGNED>::Word (&w)[3]) {
+    if (tile >= ntiles) return kNoGroup;
+    const Group which = kb == 0 ? kFirstGroup : kNextGroup;
+    if (kb == 0) {
+      int mt, nt;
+      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
+      const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r, nb = nt * (kBN / kBlock);
+      if (m < p.M)
+        ra.start(p.sa + static_cast<long long>(m) * p.kbs, p.sa, sa_bytes);
+      else
+        ra.none();
+      rb0.start(p.sw + static_cast<long long>(nb) * p.kbs, p.sw, sw_bytes);
+      rb1.start(p.sw + static_cast<long long>(min(nb + 1, last_nb)) * p.kbs, p.sw, sw_bytes);
+    }
+    w[0] = ra.next();
+    w[1] = rb0.next();
+    w[2] = rb1.next();
+    if ((kb += kGroup) >= p.kbs) {
+      kb = 0;
+      tile += tstep;
+    }
+    return which;
+  };
+  return feed_scales<3, ALIGNED>(
+      fetch, sf, r,
+      [&](uint32_t slot, uint32_t use) {
+        return use < 1 || mbar_warp_wait(&tl.sf_empty[slot], (use - 1) & 1, &tl.abort);
+      },
+      [&](uint32_t slot) {
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl.sf_full[slot], 0));
+      });
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
@@ -166,14 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* sf = ops + kStages * kStage;
-  Tail* tl = reinterpret_cast<Tail*>(sf + kSfSlots * kSfSlot);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Tail* tl = reinterpret_cast<Tail*>(sf + kSfSlots * kSfSlot + 4 * 4 * kTurn);
+  const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int tile0 = static_cast<int>(cluster_id_x()), tstep = static_cast<int>(cluster_count_x());
   const int ntiles_m = (p.M + 2 * kBM - 1) / (2 * kBM), ntiles_n = (p.N + kBN - 1) / kBN;
   const int ntiles = ntiles_m * ntiles_n;
   const int KS = p.kbs;
   volatile uint32_t* abort = &tl->abort;
+  bool issuer = false;                     // the thread that issues the MMAs
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -206,51 +370,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) {
     // ---------------- MMA issuer (the even CTA's) ----------------
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
+      issuer = true;
       constexpr uint32_t kIdesc = idesc_mx(2 * kBM, kBN);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
       const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
       uint32_t s = 0, ph = 0, it = 0, g = 0;     // operand stage, its phase; tile; scale group
       bool ok = true;
+      // group n's scales to tensor memory, buffer n % 2
+      const auto stage_scales = [&](uint32_t n) {
+        const uint32_t slot = n % kSfSlots;
+        // the MMAs that read the buffer's last contents (group n - 2) have completed
+        if (n >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(n - 2) % kSfSlots], ((n - 2) / kSfSlots) & 1, abort))
+          return false;
+        if (!mbar_wait_or_abort_cl(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) return false;
+        tc_fence_after();
+        const uint32_t t = tmem + kSfCol + (n & 1u) * kSfCols;
+        const uint64_t sd = sfdesc0 + ((slot * kSfSlot) >> 4);
+        cp_scales<true>(t, sd);
+        cp_scales<true>(t + 4, sd + (kSfBlock >> 4));
+        cp_scales<true>(t + 8, sd + (2 * kSfBlock >> 4));
+        return true;
+      };
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++it) {
         const uint32_t a = it & 1u, use = it >> 1;
         if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
         if (it >= 1 && !mbar_wait_or_abort_cl(&tl->overlap, (it - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t acc = tmem + a * kAcc1;
-        uint32_t sfa = 0;
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t j = ks & (kGroup - 1);
-          if (j == 0) {
-            const uint32_t slot = g % kSfSlots;
-            // the MMAs that read this buffer's last contents (group g - 2) have completed
-            if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            if (!mbar_wait_or_abort_cl(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
+        for (int ks0 = 0; ks0 < KS && ok; ks0 += kGroup, ++g) {
+          const uint32_t sfa = tmem + kSfCol + (g & 1u) * kSfCols;
+          if (!stage_scales(g)) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) {
+            if (!ok || ks0 + j >= KS) break;
+            if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
             tc_fence_after();
-            sfa = tmem + kSfCol + (g & 1u) * kSfCols;
-            const uint64_t sd = sfdesc0 + ((slot * kSfSlot) >> 4);
-            cp_scales<true>(sfa, sd);
-            cp_scales<true>(sfa + 4, sd + (kSfBlock >> 4));
-            cp_scales<true>(sfa + 8, sd + (2 * kSfBlock >> 4));
+            const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kStage)) >> 4);
+            const uint64_t bd = ad + (kATile >> 4);
+            const uint32_t id = kIdesc | idesc_byte(j);
+            umma_mx<true>(acc, ad, bd, id, sfa, sfa + 4, j != 0 || ks0 != 0);
+            umma_mx<true>(acc, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);     // +32 bytes = 32 values of K
+            umma_mx<true>(acc, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
+            umma_mx<true>(acc, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
+            umma_commit_pair(&tl->empty[s], 3);
+            if (++s == kStages) { s = 0; ph ^= 1u; }
           }
-          if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kStage)) >> 4);
-          const uint64_t bd = ad + (kATile >> 4);
-          const uint32_t id = kIdesc | idesc_byte(j);
-          umma_mx<true>(acc, ad, bd, id, sfa, sfa + 4, ks != 0);
-          umma_mx<true>(acc, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);     // +32 bytes = 32 values of K
-          umma_mx<true>(acc, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
-          umma_mx<true>(acc, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
-          umma_commit_pair(&tl->empty[s], 3);
-          if (++s == kStages) { s = 0; ph ^= 1u; }
-          if (j == kGroup - 1 || ks == KS - 1) {
-            umma_commit_pair(&tl->sf_empty[g % kSfSlots], 3);
-            ++g;
-          }
+          if (ok) umma_commit_pair(&tl->sf_empty[g % kSfSlots], 3);
         }
         if (ok) umma_commit_pair(&tl->acc_full[a], 3);
       }
@@ -258,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kTmaWarp) {
     // ---------------- TMA producer: each CTA its own rows, both CTAs' bytes on the even CTA's barrier ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&tmA);
       tma_prefetch_desc(&tmB);
       uint32_t s = 0, ph = 0;
@@ -282,36 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kScaleWarp) {
     // ---------------- scale loaders: this CTA's 128 rows of A, all 256 of B ----------------
-    const int r = tid - 32 * kScaleWarp;
-    const int last_nb = blocks(p.N) - 1;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
-      int mt, nt;
-      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
-      const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r;
-      const uint8_t* ra = p.sa + static_cast<long long>(m) * p.kbs;
-      const int nb = nt * (kBN / kBlock);
-      const uint8_t* rb0 = p.sw + static_cast<long long>(nb) * p.kbs;
-      const uint8_t* rb1 = p.sw + static_cast<long long>(min(nb + 1, last_nb)) * p.kbs;
-      for (int kb = 0; kb < p.kbs; kb += kGroup, ++g) {
-        const uint32_t wa = m < p.M ? scale_word(ra, kb, p.kbs, p.sf_vec) : 0u;
-        const uint32_t wb0 = scale_word(rb0, kb, p.kbs, p.sf_vec), wb1 = scale_word(rb1, kb, p.kbs, p.sf_vec);
-        const uint32_t slot = g % kSfSlots, use = g / kSfSlots;
-        if (use >= 1 && !mbar_warp_wait(&tl->sf_empty[slot], (use - 1) & 1, abort)) { ok = false; break; }
-        uint8_t* blk = sf + slot * kSfSlot;
-        put_scale_word(blk, r, wa);
-        put_scale_word(blk + kSfBlock, r, wb0);
-        put_scale_word(blk + 2 * kSfBlock, r, wb1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->sf_full[slot], 0));
-      }
-    }
+    const bool ok = p.sf_words ? load_pair_scales<true>(p, *tl, sf, rank, tile0, tstep)
+                               : load_pair_scales<false>(p, *tl, sf, rank, tile0, tstep);
     if (!ok && lane == 0) atomicOr(p.err, 32u);
   } else {
     // ---------------- epilogue ----------------
     const int r = 32 * warp + lane;         // row within this CTA's 128 rows of the tile
+    uint32_t* turn = reinterpret_cast<uint32_t*>(sf + kSfSlots * kSfSlot) + warp * kTurn;
     uint32_t it = 0;
     for (int tile = tile0; tile < ntiles; tile += tstep, ++it) {
       const uint32_t a = it & 1u, use = it >> 1;
@@ -336,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->overlap, 0));
         }
         const int nb = nt * kBN + 32 * cc;
-        if (m >= p.M || nb >= p.N) continue;
+        if (m - lane >= p.M || nb >= p.N) continue;       // the same in the whole warp
         uint16_t* dst = p.Y + static_cast<long long>(m) * p.N + nb;
         uint32_t o[16];
 #pragma unroll
@@ -345,16 +488,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
         if (nb + 32 <= p.N && p.y_vec == 2) {
-          st_v8(dst, o);
-          st_v8(dst + 16, o + 8);
+          if (m < p.M) {
+            st_v8(dst, o);
+            st_v8(dst + 16, o + 8);
+          }
         } else if (nb + 32 <= p.N && p.y_vec == 1) {
+          if (m < p.M) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
         } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (nb + j < p.N) dst[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+          put_rows(turn, lane, o, p, m - lane, nb);
         }
       }
       tc_fence_before();
@@ -366,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tl->abort) {                 // the same value in every thread after the barrier
-    drain_after_abort(warp == kMmaWarp && lane == 0 && rank == 0, &tl->drain, true);
+    drain_after_abort(issuer, &tl->drain, true);
     __syncthreads();
   }
   // Neither CTA of a pair leaves while the other may still signal its
@@ -408,6 +553,82 @@ struct __align__(8) FewTail {
 };
 static_assert(sizeof(FewTail) <= 512, "the tail fits");
 
+// The scale loaders of a CTA: its 128 weight rows, its NT tokens, K slices kb0 to kb1.
+template <int NT, bool ALIGNED>
+__device__ __forceinline__ bool load_few_scales(const Params& p, FewTail& tl, uint8_t* sf, int nt, int m0, int kb0,
+                                                int kb1) {
+  constexpr int kWords = NT > 128 ? 3 : 2;
+  const int r = threadIdx.x - 32 * kScaleWarp, lane = threadIdx.x & 31;
+  ScaleRow<ALIGNED> row[kWords];
+  row[0].start(p.sw + static_cast<long long>(nt) * p.kbs + kb0, p.sw, static_cast<long long>(blocks(p.N)) * p.kbs);
+#pragma unroll
+  for (int j = 1; j < kWords; ++j) {
+    const int t = r + 128 * (j - 1);
+    if (t < NT && m0 + t < p.M)
+      row[j].start(p.sa + static_cast<long long>(m0 + t) * p.kbs + kb0, p.sa, static_cast<long long>(p.M) * p.kbs);
+    else
+      row[j].none();
+  }
+  int kb = kb0;
+  const auto fetch = [&](typename ScaleRow<ALIGNED>::Word (&w)[kWords]) {
+    if (kb >= kb1) return kNoGroup;
+    const Group which = kb == kb0 ? kFirstGroup : kNextGroup;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = row[j].next();
+    kb += kGroup;
+    return which;
+  };
+  return feed_scales<kWords, ALIGNED>(
+      fetch, sf, r,
+      [&](uint32_t slot, uint32_t use) {
+        return use < 1 || mbar_warp_wait(&tl.sf_empty[slot], (use - 1) & 1, &tl.abort);
+      },
+      [&](uint32_t slot) {
+        if (lane == 0) mbar_arrive(&tl.sf_full[slot]);
+      });
+}
+
+// Tokens rank, rank + S, ... of the tile: a warp per token, a lane's four
+// columns from each of the cluster's S partial sums (`red`: [token][128] fp32
+// at the same place in every CTA), added in their order and written.
+template <int S>
+__device__ __forceinline__ void finish_tokens(const Params& p, uint32_t red, uint32_t rank, int m0, int n0,
+                                              int tokens) {
+  const int lane = threadIdx.x & 31, n = n0 + 4 * lane;
+  uint32_t base[S];
+#pragma unroll
+  for (int c = 0; c < S; ++c)
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[c]) : "r"(red + 16u * lane), "r"(c));
+#pragma unroll(S > 2 ? 1 : 4 / S)
+  for (int t = static_cast<int>(rank) + S * (threadIdx.x >> 5); t < tokens; t += S * (kThreads / 32)) {
+    float4 v[S];
+#pragma unroll
+    for (int c = 0; c < S; ++c)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[c].x), "=f"(v[c].y), "=f"(v[c].z), "=f"(v[c].w)
+                   : "r"(base[c] + 4u * kBM * t)
+                   : "memory");
+#pragma unroll
+    for (int c = 1; c < S; ++c) {
+      v[0].x += v[c].x;
+      v[0].y += v[c].y;
+      v[0].z += v[c].z;
+      v[0].w += v[c].w;
+    }
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y), b = __floats2bfloat162_rn(v[0].z, v[0].w);
+    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(&a), w1 = *reinterpret_cast<const uint32_t*>(&b);
+    uint16_t* dst = p.Y + static_cast<long long>(m0 + t) * p.N + n;
+    if (n + 4 <= p.N && p.y_four) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
+    } else {
+      if (n < p.N) dst[0] = static_cast<uint16_t>(w0);
+      if (n + 1 < p.N) dst[1] = static_cast<uint16_t>(w0 >> 16);
+      if (n + 2 < p.N) dst[2] = static_cast<uint16_t>(w1);
+      if (n + 3 < p.N) dst[3] = static_cast<uint16_t>(w1 >> 16);
+    }
+  }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT, const Params p) {
@@ -418,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* sf = ops + F::kRing;
   FewTail* tl = reinterpret_cast<FewTail*>(sf + kSfSlots * F::kSfSlot);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
   uint32_t rank, S;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
@@ -429,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb0 = static_cast<int>(static_cast<long long>(p.kbs) * rank / S);
   const int kb1 = static_cast<int>(static_cast<long long>(p.kbs) * (rank + 1) / S);   // S <= kbs: never empty
   volatile uint32_t* abort = &tl->abort;
+  bool issuer = false;                     // the thread that issues the MMAs
 
   if (tid == 0) {
     for (int s = 0; s < kS; ++s) {
@@ -456,43 +678,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   if (warp == kMmaWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
+      issuer = true;
       constexpr uint32_t kIdesc = idesc_mx(kBM, NT);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
       const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
-      uint32_t s = 0, ph = 0, g = 0, sfa = 0;
+      uint32_t s = 0, ph = 0, g = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const uint32_t j = (kb - kb0) & (kGroup - 1);
-        if (j == 0) {
-          const uint32_t slot = g % kSfSlots;
-          if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_or_abort(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
-          tc_fence_after();
-          sfa = tmem + F::kSfCol + (g & 1u) * F::kSfCols;
-          const uint64_t sd = sfdesc0 + ((slot * F::kSfSlot) >> 4);
-          cp_scales<false>(sfa, sd);
-          cp_scales<false>(sfa + 4, sd + (kSfBlock >> 4));
-          if constexpr (NT > 128) cp_scales<false>(sfa + 8, sd + (2 * kSfBlock >> 4));
+      for (int kg = kb0; kg < kb1 && ok; kg += kGroup, ++g) {
+        const uint32_t slot = g % kSfSlots;
+        if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
+          ok = false;
+          break;
         }
-        if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+        if (!mbar_wait_or_abort(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(F::kStage)) >> 4);
-        const uint64_t bd = ad + (F::kWTile >> 4);
-        const uint32_t id = kIdesc | idesc_byte(j);
-        umma_mx<false>(tmem, ad, bd, id, sfa, sfa + 4, kb != kb0);
-        umma_mx<false>(tmem, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);
-        umma_mx<false>(tmem, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
-        umma_mx<false>(tmem, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
-        umma_commit(&tl->empty[s]);
-        if (++s == kS) { s = 0; ph ^= 1u; }
-        if (j == kGroup - 1 || kb == kb1 - 1) {
-          umma_commit(&tl->sf_empty[g % kSfSlots]);
-          ++g;
+        const uint32_t sfa = tmem + F::kSfCol + (g & 1u) * F::kSfCols;
+        const uint64_t sd = sfdesc0 + ((slot * F::kSfSlot) >> 4);
+        cp_scales<false>(sfa, sd);
+        cp_scales<false>(sfa + 4, sd + (kSfBlock >> 4));
+        if constexpr (NT > 128) cp_scales<false>(sfa + 8, sd + (2 * kSfBlock >> 4));
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          if (!ok || kg + j >= kb1) break;
+          if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(F::kStage)) >> 4);
+          const uint64_t bd = ad + (F::kWTile >> 4);
+          const uint32_t id = kIdesc | idesc_byte(j);
+          umma_mx<false>(tmem, ad, bd, id, sfa, sfa + 4, j != 0 || kg != kb0);
+          umma_mx<false>(tmem, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);
+          umma_mx<false>(tmem, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
+          umma_mx<false>(tmem, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
+          umma_commit(&tl->empty[s]);
+          if (++s == kS) { s = 0; ph ^= 1u; }
         }
+        if (ok) umma_commit(&tl->sf_empty[slot]);
       }
       if (ok)
         umma_commit(&tl->acc_full);
@@ -500,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(p.err, 2u);
     }
   } else if (warp == kTmaWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&tmW);
       tma_prefetch_desc(&tmT);
       uint32_t s = 0, ph = 0;
@@ -516,27 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) atomicOr(p.err, 16u);
     }
   } else if (warp >= kScaleWarp) {
-    const int r = tid - 32 * kScaleWarp;
-    const uint8_t* rw = p.sw + static_cast<long long>(nt) * p.kbs;
-    const uint8_t* rt0 = p.sa + static_cast<long long>(m0 + r) * p.kbs;
-    const uint8_t* rt1 = rt0 + 128ll * p.kbs;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int kb = kb0; kb < kb1; kb += kGroup, ++g) {
-      const bool vec = p.sf_vec && (kb & 3) == 0;
-      const uint32_t ww = scale_word(rw, kb, kb1, vec);
-      const uint32_t w0 = r < NT && m0 + r < p.M ? scale_word(rt0, kb, kb1, vec) : 0u;
-      const uint32_t w1 = NT > 128 && m0 + r + 128 < p.M ? scale_word(rt1, kb, kb1, vec) : 0u;
-      const uint32_t slot = g % kSfSlots, use = g / kSfSlots;
-      if (use >= 1 && !mbar_warp_wait(&tl->sf_empty[slot], (use - 1) & 1, abort)) { ok = false; break; }
-      uint8_t* blk = sf + slot * F::kSfSlot;
-      put_scale_word(blk, r, ww);
-      put_scale_word(blk + kSfBlock, r, w0);
-      if constexpr (NT > 128) put_scale_word(blk + 2 * kSfBlock, r, w1);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tl->sf_full[slot]);
-    }
+    const bool ok = p.sf_words ? load_few_scales<NT, true>(p, *tl, sf, nt, m0, kb0, kb1)
+                               : load_few_scales<NT, false>(p, *tl, sf, nt, m0, kb0, kb1);
     if (!ok && lane == 0) atomicOr(p.err, 32u);
   } else {
     // partial sums -> red[token][128 columns] where the operands were: every
@@ -564,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const bool failed = tl->abort != 0u;
   if (failed) {
-    drain_after_abort(warp == kMmaWarp && lane == 0, &tl->drain);
+    drain_after_abort(issuer, &tl->drain);
     __syncthreads();
   }
   if (warp == kMmaWarp) {
@@ -575,23 +777,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // `rank` finishes tokens rank, rank + S, ...
   if (S > 1) cluster_sync();
   const int tokens = min(NT, p.M - m0);
-  if (tid < 256) {
-    const int n = tid & 127;
-    const uint32_t mine = smem_u32(ops) + 4u * n;
-    if (n0 + n < p.N) {
-      for (int t = static_cast<int>(rank) + static_cast<int>(S) * (tid >> 7); t < tokens; t += 2 * static_cast<int>(S)) {
-        float sum = 0.f;
-        for (uint32_t c = 0; c < S; ++c) {
-          uint32_t addr;
-          float v;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(mine + 4u * kBM * t), "r"(c));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-          sum += v;
-        }
-        p.Y[static_cast<long long>(m0 + t) * p.N + n0 + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
-      }
-    }
-  }
+  const uint32_t red = smem_u32(ops);
+  if (S == 1)
+    finish_tokens<1>(p, red, 0, m0, n0, tokens);
+  else if (S == 2)
+    finish_tokens<2>(p, red, rank, m0, n0, tokens);
+  else if (S == 4)
+    finish_tokens<4>(p, red, rank, m0, n0, tokens);
+  else
+    finish_tokens<8>(p, red, rank, m0, n0, tokens);
   __syncwarp();
   if (S > 1) cluster_sync();       // no CTA leaves while another reads its sums
 }
@@ -675,7 +869,7 @@ int launch_pair(const uint8_t* a, const uint8_t* w, Params p, int dev, cudaStrea
 }
 
 template <int NT>
-int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int dev, int sms, cudaStream_t st) {
+int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int dev, cudaStream_t st) {
   using F = Few<NT>;
   static bool ready[kMaxDevices] = {};
   if (!ready[dev]) {
@@ -685,9 +879,6 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int dev, int
     ready[dev] = true;
   }
   const long long ntiles = static_cast<long long>(blocks(p.N)) * ((p.M + NT - 1) / NT);
-  // K split over a cluster while the SMs are not all in use and each part keeps two slices or more
-  int S = 1;
-  while (S < 8 && ntiles * S * 2 <= sms && p.kbs >= 4 * S) S *= 2;
   if (ntiles * S > 0x7FFFFFFFll) return RBQ_EINVAL;
   CUtensorMap mW, mT;
   int rc = encode_map(&mW, w, p.N, p.K, kBM);
@@ -704,6 +895,44 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int dev, int
   cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_few_kernel<NT>, mW, mT, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+}
+
+// Which kernel, with how many tokens to a tile and how many CTAs to a tile's
+// K: what takes least by a linear model, in ns, of the times of 24 layers of 1 to
+// 4096 tokens, 64 to 16384 outputs and 256 to 16384 inputs with every choice
+// of both (its choice was the best or within 6 % of it in all of them):
+//   a launch `start[NT]`, a K slice `slice[NT]`, each further wave of CTAs `wave`, a
+//   cluster's joint sum 600 + 200 S + 8 NT.
+// Few tokens to a tile fill the GPU and share little; the pair kernel shares
+// most and pays from about 100 tiles of 256 x 256.  For instance 512 x 4096 x
+// 4096: 17.4 us by pairs, 11.1 with NT = 128 (S = 1), 13.3 with NT = 256 and S = 2; 1 x 4096 x
+// 4096: 5.3 us with S = 4, 6.7 with S = 1; 4096 x 4096 x 4096: 57.6 us by pairs, 65.4 with
+// NT = 256; 333 x 1001 x 1552: 5.9 us with NT = 32, 13.7 by pairs.
+struct Plan {
+  int NT, S;                // tokens to a tile (0: the pair kernel), CTAs to a cluster
+};
+Plan make_plan(int M, int N, int kbs, int sms) {
+  const auto waves = [](long long tiles, int n) { return (tiles + n - 1) / n; };
+  const long long pair_waves = waves(((M + 255LL) / 256) * ((N + 255LL) / 256), sms / 2);
+  Plan best{0, 1};
+  long long least = 6700 + 1900 * (pair_waves - 1) + 340 * pair_waves * kbs;
+  constexpr struct {
+    int NT, start, slice;
+  } kinds[] = {{16, 2300, 150}, {32, 2750, 150}, {64, 2750, 190}, {128, 3300, 212}, {256, 6900, 270}};
+  for (const auto& k : kinds) {
+    const long long tiles = static_cast<long long>(blocks(N)) * ((M + k.NT - 1LL) / k.NT);
+    for (int S = 1; S <= 8 && S <= kbs; S *= 2) {
+      const long long w = waves(tiles * S, sms);
+      const long long t = k.start + 5000 * (w - 1) + w * ((kbs + S - 1) / S) * k.slice +
+                          (S > 1 ? 600 + 200 * S + 8 * k.NT : 0);
+      if (t < least) {
+        least = t;
+        best = {k.NT, S};
+      }
+    }
+    if (k.NT >= M) break;
+  }
+  return best;
 }
 
 }  // namespace
@@ -726,7 +955,8 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
   p.sa = a_scales;
   p.sw = w_scales;
   p.Y = Y;
-  p.sf_vec = p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4);
+  p.sf_words = p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4);
+  p.y_four = N % 4 == 0 && aligned(Y, 8);
   p.y_vec = N % 16 == 0 && aligned(Y, 32) ? 2 : N % 8 == 0 && aligned(Y, 16) ? 1 : 0;
   int rc = device_error_word_ptr(&p.err);
   if (rc != RBQ_OK) return rc;
@@ -736,10 +966,15 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
   if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (M <= 16) return fp8::launch_few<16>(a_codes, w_codes, p, dev, sms, st);
-  if (M <= 32) return fp8::launch_few<32>(a_codes, w_codes, p, dev, sms, st);
-  if (M <= 64) return fp8::launch_few<64>(a_codes, w_codes, p, dev, sms, st);
-  if (M <= 128) return fp8::launch_few<128>(a_codes, w_codes, p, dev, sms, st);
-  if (M <= 256) return fp8::launch_few<256>(a_codes, w_codes, p, dev, sms, st);
+  const fp8::Plan plan = fp8::make_plan(M, N, p.kbs, sms);
+  const int S = plan.S;
+  for (int r = 1; r < S; ++r) p.sf_words = p.sf_words && static_cast<long long>(p.kbs) * r / S % 4 == 0;
+  switch (plan.NT) {
+    case 16: return fp8::launch_few<16>(a_codes, w_codes, p, S, dev, st);
+    case 32: return fp8::launch_few<32>(a_codes, w_codes, p, S, dev, st);
+    case 64: return fp8::launch_few<64>(a_codes, w_codes, p, S, dev, st);
+    case 128: return fp8::launch_few<128>(a_codes, w_codes, p, S, dev, st);
+    case 256: return fp8::launch_few<256>(a_codes, w_codes, p, S, dev, st);
+  }
   return fp8::launch_pair(a_codes, w_codes, p, dev, st);
 }
