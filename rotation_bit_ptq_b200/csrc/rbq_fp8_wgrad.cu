@@ -11,8 +11,8 @@
 // Two kernels per call (three when the tokens are split):
 // 1. decode_rows_kernel: codes and scales -> BF16 [M, K] in a stream-ordered
 //    workspace.
-// 2. wgrad_kernel: persistent, on CTA pairs, 256 x 256 tiles of dW
-//    (cta_group::2), slices of 64 tokens.  Both operands lie with the token
+// 2. wgrad_kernel: persistent, on CTA pairs, tiles of 256 x 256 or 256 x 128
+//    values of dW (cta_group::2), slices of 64 tokens.  Both operands lie with the token
 //    as their row, so they are "MN-major": a TMA box of 64 tokens x 64
 //    columns (128 bytes, 128B swizzle) is one column of swizzle atoms.  Warps
 //    0..3 epilogue, 4 MMA issuer, 5 TMA producer.
@@ -22,6 +22,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+
+#include <utility>
 
 #include "rbq_fp8.cuh"
 #include "rbq_internal.h"
@@ -36,18 +38,25 @@ namespace {
 using namespace sm100;
 
 constexpr int kTok = 64;                   // tokens per slice
-constexpr int kTile = 256;                 // rows and columns of dW per tile
-constexpr int kHalf = 128;                 // of them per CTA and operand
+constexpr int kTileN = 256;                // rows of dW per tile
+constexpr int kHalf = kTileN / 2;          // of them per CTA
 constexpr int kBox = 64;                   // columns per TMA box (128 bytes)
 constexpr int kBoxBytes = kBox * 2 * kTok; // 8 KB
-constexpr int kOperand = kHalf / kBox * kBoxBytes;   // 16 KB
-constexpr int kWStage = 2 * kOperand;
-constexpr int kWStages = 6;
 constexpr int kWThreads = 192;
 constexpr int kWMmaWarp = 4, kWTmaWarp = 5;
 
-// Instruction descriptor: BF16 A and B, both MN-major (bits 15 and 16), fp32 sums.
-constexpr uint32_t kWIdesc = idesc_f16(kTile, kTile, true) | (1u << 15) | (1u << 16);
+// Tiles of 256 x BK (256 or 128) values of dW.
+template <int BK>
+struct Wg {
+  static constexpr int kA = kHalf / kBox * kBoxBytes;         // dY: 16 KB per CTA
+  static constexpr int kB = BK / 2 / kBox * kBoxBytes;        // x: 16 or 8 KB
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = BK == 256 ? 6 : 8;
+  static constexpr uint32_t kTmemCols = 2 * BK;
+  // Instruction descriptor: BF16 A and B, both MN-major (bits 15 and 16), fp32 sums.
+  static constexpr uint32_t kIdesc = idesc_f16(kTileN, BK, true) | (1u << 15) | (1u << 16);
+};
+constexpr int kWMaxStages = 8;
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle
 // layout: 64 columns x 8 tokens per swizzle atom; the next 8 tokens 1024
@@ -69,8 +78,8 @@ struct WParams {
 };
 
 struct __align__(8) WTail {
-  uint64_t full[kWStages];
-  uint64_t empty[kWStages];
+  uint64_t full[kWMaxStages];
+  uint64_t empty[kWMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
@@ -78,7 +87,8 @@ struct __align__(8) WTail {
   volatile uint32_t abort;
 };
 
-constexpr size_t kWSmem = 1024 + kWStages * kWStage + sizeof(WTail) + 64;
+template <int BK>
+constexpr size_t kWSmem = 1024 + Wg<BK>::kStages * Wg<BK>::kStage + sizeof(WTail) + 64;
 
 __device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
@@ -92,19 +102,23 @@ __device__ __forceinline__ void part_range(int slices, int parts, int part, int&
   last = static_cast<int>(static_cast<long long>(slices) * (part + 1) / parts);
 }
 
+template <int BK>
 __global__ void __launch_bounds__(kWThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX, const WParams p) {
+  using G = Wg<BK>;
+  constexpr int kWStages = G::kStages, kWStage = G::kStage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   WTail* tl = reinterpret_cast<WTail*>(ops + kWStages * kWStage);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int work0 = static_cast<int>(cluster_id_x()), wstep = static_cast<int>(cluster_count_x());
-  const int ntiles_n = (p.N + kTile - 1) / kTile, ntiles_k = (p.K + kTile - 1) / kTile;
+  const int ntiles_n = (p.N + kTileN - 1) / kTileN, ntiles_k = (p.K + BK - 1) / BK;
   const int ntiles = ntiles_n * ntiles_k, nwork = ntiles * p.parts;
   const int slices = (p.M + kTok - 1) / kTok;
   volatile uint32_t* abort = &tl->abort;
+  bool issuer = false;                     // the thread that issues the MMAs
 
   if (tid == 0) {
     for (int s = 0; s < kWStages; ++s) {
@@ -120,7 +134,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     mbar_fence_init();
   }
   if (warp == kWMmaWarp) {
-    tmem_alloc_pair(&tl->tmem_slot, 512);
+    tmem_alloc_pair(&tl->tmem_slot, G::kTmemCols);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -131,7 +145,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   griddep_launch_dependents();
 
   if (warp == kWMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
+      issuer = true;
       const uint64_t desc0 = sdesc_mn_sw128(smem_u32(ops));
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
@@ -139,17 +154,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const uint32_t a = it & 1u, use = it >> 1;
         if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t acc = tmem + a * kTile;
+        const uint32_t acc = tmem + a * BK;
         int first, last;
         part_range(slices, p.parts, w / ntiles, first, last);
         for (int t = first; t < last; ++t) {
           if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kWStage)) >> 4);
-          const uint64_t bd = ad + (kOperand >> 4);
+          const uint64_t bd = ad + (G::kA >> 4);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)          // 16 tokens = two atoms of 8
-            umma_f16_pair(acc, ad + k * (2048 >> 4), bd + k * (2048 >> 4), kWIdesc, t != first || k != 0);
+            umma_f16_pair(acc, ad + k * (2048 >> 4), bd + k * (2048 >> 4), G::kIdesc, k != 0 || t != first);
           umma_commit_pair(&tl->empty[s], 3);
           if (++s == kWStages) { s = 0; ph ^= 1u; }
         }
@@ -158,7 +173,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (!ok) atomicOr(p.err, 2u);
     }
   } else if (warp == kWTmaWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&tmY);
       tma_prefetch_desc(&tmX);
       uint32_t s = 0, ph = 0;
@@ -167,17 +182,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
         int nt, kt, first, last;
         tiles::tile_coords(w % ntiles, ntiles_n, ntiles_k, p.order, nt, kt);
         part_range(slices, p.parts, w / ntiles, first, last);
-        const int n0 = nt * kTile + static_cast<int>(rank) * kHalf, k0 = kt * kTile + static_cast<int>(rank) * kHalf;
+        const int n0 = nt * kTileN + static_cast<int>(rank) * kHalf, k0 = kt * BK + static_cast<int>(rank) * (BK / 2);
         for (int t = first; t < last; ++t) {
           if (wrapped && !mbar_wait_or_abort(&tl->empty[s], ph ^ 1u, abort)) { ok = false; break; }
           uint8_t* st = ops + s * kWStage;
           if (rank == 0) mbar_arrive_expect_tx(&tl->full[s], 2 * kWStage);
           const uint32_t bar = mapa_shared(&tl->full[s], 0);
 #pragma unroll
-          for (int b = 0; b < kHalf / kBox; ++b) {
+          for (int b = 0; b < kHalf / kBox; ++b)
             tma_load_2d_pair(st + b * kBoxBytes, &tmY, n0 + b * kBox, t * kTok, bar);
-            tma_load_2d_pair(st + kOperand + b * kBoxBytes, &tmX, k0 + b * kBox, t * kTok, bar);
-          }
+#pragma unroll
+          for (int b = 0; b < BK / 2 / kBox; ++b)
+            tma_load_2d_pair(st + G::kA + b * kBoxBytes, &tmX, k0 + b * kBox, t * kTok, bar);
           if (++s == kWStages) { s = 0; ph ^= 1u; wrapped = true; }
         }
       }
@@ -195,14 +211,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
       tc_fence_after();
       int nt, kt;
       tiles::tile_coords(w % ntiles, ntiles_n, ntiles_k, p.order, nt, kt);
-      const int n = nt * kTile + static_cast<int>(rank) * kHalf + r;
+      const int n = nt * kTileN + static_cast<int>(rank) * kHalf + r;
       const long long row = static_cast<long long>(w / ntiles) * p.N + n;
 #pragma unroll 1
-      for (int cc = 0; cc < kTile / 32; ++cc) {
+      for (int cc = 0; cc < BK / 32; ++cc) {
         uint32_t v[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * kTile + 32 * cc, v);
+        tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * BK + 32 * cc, v);
         tmem_wait_ld();
-        const int kc = kt * kTile + 32 * cc;
+        const int kc = kt * BK + 32 * cc;
         if (n >= p.N || kc >= p.K) continue;
         const int left = p.K - kc;                      // a multiple of 16
         if (p.f32) {
@@ -243,25 +259,29 @@ __global__ void __launch_bounds__(kWThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tl->abort) {
-    drain_after_abort(warp == kWMmaWarp && lane == 0 && rank == 0, &tl->drain, true);
+    drain_after_abort(issuer, &tl->drain, true);
     __syncthreads();
   }
   cluster_sync();
   if (warp == kWMmaWarp) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, G::kTmemCols);
   }
 }
 
-// Codes and scales -> BF16 values, 16 per thread (K is a multiple of 16).
-__global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, const uint8_t* scales, long long pieces,
-                                                          int K, int kbs, uint16_t* out) {
-  const int per_row = K / 16;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < pieces; i += 256ll * gridDim.x) {
-    const long long row = i / per_row;
-    const int col = static_cast<int>(i - row * per_row) * 16;
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-    const float s = scale_value(__ldg(scales + row * kbs + col / kBlock));
+// Codes and scales -> BF16 values, 16 per thread (K is a multiple of 16); CTA
+// (x, y): 4096 values of each of `rows` rows from row `rows` y on.
+__global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, const uint8_t* scales, int M, int K,
+                                                          int kbs, int rows, uint16_t* out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int col = (blockIdx.x * 256 + threadIdx.x) * 16, row0 = blockIdx.y * rows, row1 = min(M, row0 + rows);
+  if (col >= K) return;
+#pragma unroll 4
+  for (int row = row0; row < row1; ++row) {
+    const long long at = static_cast<long long>(row) * K + col;
+    const uint4 c = *reinterpret_cast<const uint4*>(codes + at);
+    const float s = scale_value(scales[static_cast<long long>(row) * kbs + col / kBlock]);
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t o[8];
 #pragma unroll
@@ -270,31 +290,32 @@ __global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, 
       const __nv_bfloat162 h = __floats2bfloat162_rn(v.x * s, v.y * s);      // exact
       o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + 16 * i);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    st_v8(out + at, o);                     // the workspace and its rows are 32-byte aligned
   }
 }
 
 // out[i] = part 0 + part 1 + ... in that order.
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int nparts, long long n4, void* out,
                                                         int f32) {
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += 256ll * gridDim.x) {
-    float4 s = parts[i];
-    for (int q = 1; q < nparts; ++q) {
-      const float4 v = parts[q * n4 + i];
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    if (f32) {
-      static_cast<float4*>(out)[i] = s;
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
-      static_cast<uint2*>(out)[i] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
+  if (i >= n4) return;
+  float4 s = parts[i];
+#pragma unroll 8
+  for (int q = 1; q < nparts; ++q) {
+    const float4 v = parts[q * n4 + i];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  if (f32) {
+    static_cast<float4*>(out)[i] = s;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+    static_cast<uint2*>(out)[i] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 }
 
@@ -313,18 +334,19 @@ int encode_tokens_map(CUtensorMap* map, const uint16_t* base, int rows, int cols
 }
 
 // Pairs of wgrad_kernel that can be resident on device `dev`, asked once per device (0: none).
+template <int BK>
 int wgrad_pairs(int dev) {
   static int cached[kMaxDevices] = {};        // 0 = not yet asked; else pairs + 1
   if (cached[dev]) return cached[dev] - 1;
-  if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kWSmem)) !=
-      cudaSuccess) {
+  if (cudaFuncSetAttribute(wgrad_kernel<BK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kWSmem<BK>)) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kWThreads, 1, 1);
-  cfg.dynamicSmemBytes = kWSmem;
+  cfg.dynamicSmemBytes = kWSmem<BK>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -333,7 +355,7 @@ int wgrad_pairs(int dev) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, wgrad_kernel, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, wgrad_kernel<BK>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -341,20 +363,76 @@ int wgrad_pairs(int dev) {
   return n;
 }
 
+// Launches that may set themselves up while the one before them runs (each
+// waits for its end before it touches memory); `pair`: clusters of two CTAs.
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool pair, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+}
+
+// The width of a tile and the parts the tokens are split into: what takes
+// least by a linear model, in ns, of the times of 15 gradients of 16 to 32760
+// tokens and 64 x 128 to 16384 x 4096 weights (its choice was the best or
+// within 7 % of it): `start` a launch, `slice` each 64 tokens, `wave` each
+// further wave of tiles, and for the joint sum 2300, 110 a part and 0.3 per
+// thousand fp32 values moved.  Narrow tiles are twice as many, wide ones read dY half as
+// often: 1560 x 1536 x 1536 takes 11.7 us with 128 (no parts), 15.9 with 256 and
+// 17.3 with 256 in two parts; 4096 x 16384 x 4096 332 us with 256, 366 with
+// 128; 3001 x 64 x 128 9.6 us in 5 parts, 13.1 in one.
+struct WPlan {
+  int BK, parts;
+};
+WPlan make_wplan(int M, int N, int K, int pairs) {
+  const auto waves = [](long long tiles, int n) { return (tiles + n - 1) / n; };
+  constexpr struct {
+    int BK, start, wave, slice;
+  } kinds[] = {{256, 4700, 2600, 310}, {128, 3600, 1300, 165}};
+  const int slices = (M + kTok - 1) / kTok;
+  WPlan best{256, 1};
+  long long least = -1;
+  for (const auto& k : kinds) {
+    const long long ntiles = ((N + 255LL) / 256) * ((K + k.BK - 1LL) / k.BK);
+    for (int parts = 1; parts <= slices && (parts == 1 || ntiles * parts <= pairs); ++parts) {
+      const long long w = waves(ntiles * parts, pairs);
+      const long long t = k.start + k.wave * (w - 1) + w * waves(slices, parts) * k.slice +
+                          (parts > 1 ? 2300 + 110 * parts + (parts + 1LL) * N * K * 3 / 10000 : 0);
+      if (least < 0 || t < least) {
+        least = t;
+        best = {k.BK, parts};
+      }
+    }
+  }
+  return best;
+}
+
 int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M, int N, int K, void* dW, bool f32,
           unsigned int* err, cudaStream_t st) {
-  int dev = 0, sms = 148;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int pairs = wgrad_pairs(dev);
-  if (pairs < 1) return RBQ_ECUDA;
-  const long long ntiles = ((N + kTile - 1LL) / kTile) * ((K + kTile - 1LL) / kTile);
-  if (ntiles > (1 << 24)) return RBQ_EINVAL;
-  const int slices = (M + kTok - 1) / kTok;
-  int parts = 1;
-  while (ntiles * (parts + 1) <= pairs && slices >= 4 * (parts + 1)) ++parts;
+  const int pairs256 = wgrad_pairs<256>(dev), pairs128 = wgrad_pairs<128>(dev);
+  if (pairs256 < 1 || pairs128 < 1) return RBQ_ECUDA;
+  const WPlan plan = make_wplan(M, N, K, pairs256);
+  const int parts = plan.parts, pairs = plan.BK == 256 ? pairs256 : pairs128;
+  const long long ntiles = ((N + kTileN - 1LL) / kTileN) * ((K + plan.BK - 1LL) / plan.BK);
+  if (ntiles * parts > (1 << 28)) return RBQ_EINVAL;
 
   cudaMemPool_t pool = qfast::workspace_pool(dev);
   if (!pool) return RBQ_ECUDA;
@@ -366,12 +444,13 @@ int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M
   uint16_t* x = static_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + x_bytes);
 
-  const long long pieces = static_cast<long long>(M) * (K / 16);
-  long long grid = (pieces + 255) / 256;
-  if (grid > 16LL * sms) grid = 16LL * sms;
-  decode_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(codes, scales, pieces, K, blocks(K), x);
-  e = cudaGetLastError();
-  int rc = e == cudaSuccess ? RBQ_OK : cuda_fail(e);
+  // rows per CTA: enough CTAs to fill the GPU, at most 65535 along y
+  const int xs = (K + 4095) / 4096;
+  int rows = 1;
+  while (rows < 8 && static_cast<long long>(xs) * M / (2 * rows) >= 148 * 8) rows *= 2;
+  while ((M + rows - 1) / rows > 65535) rows *= 2;
+  int rc = launch(decode_rows_kernel, dim3(xs, (M + rows - 1) / rows, 1), 256, 0, false, st, codes, scales, M, K,
+                  blocks(K), rows, x);
 
   WParams p{};
   p.M = M;
@@ -388,32 +467,16 @@ int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M
   if (rc == RBQ_OK) rc = encode_tokens_map(&mX, x, M, K);
   if (rc == RBQ_OK) {
     const long long nwork = ntiles * parts;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * static_cast<unsigned>(nwork < pairs ? nwork : pairs), 1, 1);
-    cfg.blockDim = dim3(kWThreads, 1, 1);
-    cfg.dynamicSmemBytes = kWSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, wgrad_kernel, mY, mX, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) rc = cuda_fail(e);
+    const dim3 grid(2 * static_cast<unsigned>(nwork < pairs ? nwork : pairs), 1, 1);
+    rc = plan.BK == 256 ? launch(wgrad_kernel<256>, grid, kWThreads, kWSmem<256>, true, st, mY, mX, p)
+                        : launch(wgrad_kernel<128>, grid, kWThreads, kWSmem<128>, true, st, mY, mX, p);
   }
   if (rc == RBQ_OK && parts > 1) {
-    const long long n4 = static_cast<long long>(N) * K / 4;
-    long long g = (n4 + 255) / 256;
-    if (g > 16LL * sms) g = 16LL * sms;
-    sum_parts_kernel<<<static_cast<unsigned>(g), 256, 0, st>>>(reinterpret_cast<const float4*>(part), parts, n4, dW,
-                                                               f32);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) rc = cuda_fail(e);
+    const long long n4 = static_cast<long long>(N) * K / 4, grid = (n4 + 255) / 256;
+    rc = grid > 0x7FFFFFFFll
+             ? RBQ_EINVAL
+             : launch(sum_parts_kernel, dim3(static_cast<unsigned>(grid), 1, 1), 256, 0, false, st,
+                      reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
   }
   e = cudaFreeAsync(ws, st);
   if (rc == RBQ_OK && e != cudaSuccess) rc = cuda_fail(e);
