@@ -23,12 +23,17 @@ namespace {
 using sm100::griddep_launch_dependents;
 using sm100::griddep_wait;
 
-// A thread holds 16 consecutive values of a row (d is a multiple of 16); the
-// 8 threads of a block of 128 find its maximum by shuffles.
-constexpr int kVals = 16;
+// The row kernels: a thread holds 32 consecutive values of a row (of which the
+// second 16 may lie behind its end: d is a multiple of 16), and the 4 threads of a
+// block of 128 find its maximum by shuffles.  What a thread does besides its
+// values (its place, shuffles, scales) is paid half as often as with 16
+// values: 32760 x 8960 with GELU and checkpoint took 243 us with 16 values, 223 with
+// 32 in CTAs of 256 threads and 207 in CTAs of 128, eight to an SM.
+constexpr int kVals = 32;
+constexpr int kRowThreads = 128, kRowCtas = 8;
 constexpr int kLanesPerBlock = kBlock / kVals;
-constexpr int kThreads = 256;
-constexpr int kBlocksPerCta = kThreads / kLanesPerBlock;
+constexpr int kBlocksPerCta = kRowThreads / kLanesPerBlock;
+constexpr int kWeightThreads = 256;
 constexpr uint32_t kNaN = 0x7FFFFFFFu;
 
 // ---- pairs of fp32 in one 64-bit register, for the packed FMA ------------------
@@ -82,20 +87,26 @@ __device__ __forceinline__ void store32(void* dst, bool wide, const uint32_t* w)
   }
 }
 
-// Sixteen values of a row as they are stored: 8 words of two BF16, or 16 of one fp32.
-template <typename T>
+// V values of a row as they are stored: words of two BF16 or of one fp32.
+template <typename T, int V>
 struct Piece {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWords = kF32 ? 16 : 8;
+  static constexpr int kPairs = V / 2, kHalfWords = kF32 ? 16 : 8, kWords = V / 16 * kHalfWords;
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void zero() {
+  // The first `n` values (a multiple of 16); the others are 0.
+  __device__ __forceinline__ void load(const T* src, int n, bool wide) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ void load(const T* src, bool wide) {
-    load32(src, wide, w);
-    if constexpr (kF32) load32(src + 8, wide, w + 8);
+    for (int h = 0; h < V / 16; ++h) {
+      uint32_t* u = w + h * kHalfWords;
+      if (16 * h < n) {
+        load32(src + 16 * h, wide, u);
+        if constexpr (kF32) load32(src + 16 * h + 8, wide, u + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHalfWords; ++i) u[i] = 0u;
+      }
+    }
   }
   __device__ __forceinline__ f2 pair(int i) const {
     if constexpr (kF32)
@@ -108,13 +119,13 @@ struct Piece {
     if constexpr (kF32) {
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2)
+      for (int i = 0; i < V; i += 2)
         m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i])), fabsf(__uint_as_float(w[i + 1]))));
       return m;
     } else {
-      __nv_bfloat162 m = __habs2(half_pair(0));
+      __nv_bfloat162 m = __habs2(two(0));
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(half_pair(i)));
+      for (int i = 1; i < kWords; ++i) m = __hmax2(m, __habs2(two(i)));
       return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
     }
   }
@@ -131,18 +142,18 @@ struct Piece {
   }
 
  private:
-  __device__ __forceinline__ __nv_bfloat162 half_pair(int i) const {
-    return *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-  }
+  __device__ __forceinline__ __nv_bfloat162 two(int i) const { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); }
 };
-// Sixteen values as pairs of fp32.
+// V values as pairs of fp32.
+template <int V>
 struct Pairs {
-  f2 v[kVals / 2];
+  static constexpr int kPairs = V / 2;
+  f2 v[kPairs];
   __device__ __forceinline__ f2 pair(int i) const { return v[i]; }
   __device__ __forceinline__ float amax() const {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < kVals / 2; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       float a, b;
       unpack(v[i], a, b);
       m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
@@ -151,7 +162,7 @@ struct Pairs {
   }
   __device__ __forceinline__ void drop_infinities() {
 #pragma unroll
-    for (int i = 0; i < kVals / 2; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       float a, b;
       unpack(v[i], a, b);
       if (fabsf(a) == INFINITY) a = __uint_as_float(kNaN);
@@ -161,14 +172,14 @@ struct Pairs {
   }
 };
 
-// Maximum over the 8 threads of a block (every lane of the warp takes part).
+// Maximum over the threads of a block (every lane of the warp takes part).
 __device__ __forceinline__ float block_max(float m) {
 #pragma unroll
   for (int o = kLanesPerBlock / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-// The scale byte of the block this thread's 16 values belong to.  An infinity
+// The scale byte of the block this thread's values belong to.  An infinity
 // has no E4M3 value: it becomes NaN (and so reaches the result) and does not
 // count for the maximum, which would otherwise flush its 127 neighbours.
 template <typename V>
@@ -182,17 +193,15 @@ __device__ __forceinline__ uint32_t block_scale(V& x) {
 }
 
 template <typename V>
-__device__ __forceinline__ uint4 encode16(const V& x, float inv) {
+__device__ __forceinline__ void encode(const V& x, float inv, uint32_t (&w)[V::kPairs / 2]) {
   const f2 k = both(inv);
-  uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < V::kPairs / 2; ++j) {
     float a, b, c, d;
     unpack(mul2(x.pair(2 * j), k), a, b);
     unpack(mul2(x.pair(2 * j + 1), k), c, d);
     w[j] = encode4(a, b, c, d);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---- the GELU --------------------------------------------------------------------
@@ -243,17 +252,19 @@ __device__ __forceinline__ f2 gelu_slope(f2 x) {
   return pack(a >= 0.f ? h0 : g0, b >= 0.f ? h1 : g1);
 }
 
-// ---- where a group of 8 threads works ---------------------------------------------
+// ---- where a block's threads work ----------------------------------------------------
 struct Rows {
   long long total;        // blocks of 128 in all
   int d, kbs;
   uint32_t mul;           // b / kbs = (b mul) >> shift for b < 2^31
   int shift;
   int wide;               // 32-byte accesses to the 16-bit (or fp32) rows
+  int wide_codes;         // ... and to the codes
 };
 struct Place {
   long long off, so;      // this thread's first value, the block's scale
-  bool in, lead;
+  int n;                  // its values: 32, 16 or none
+  bool lead;
 };
 __device__ __forceinline__ Place place(const Rows& r) {
   const long long b = static_cast<long long>(blockIdx.x) * kBlocksPerCta + threadIdx.x / kLanesPerBlock;
@@ -263,66 +274,78 @@ __device__ __forceinline__ Place place(const Rows& r) {
   const int sub = threadIdx.x % kLanesPerBlock;
   const int col = static_cast<int>(b - row * r.kbs) * kBlock + sub * kVals;
   Place p;
-  p.in = b < r.total && col < r.d;                    // the last block of a row may be short
-  p.lead = sub == 0 && p.in;
+  p.n = b < r.total ? min(max(r.d - col, 0), kVals) : 0;          // the last block of a row may be short
+  p.lead = sub == 0 && b < r.total;
   p.off = row * r.d + col;
   p.so = b;
   return p;
 }
+__device__ __forceinline__ void store_codes(uint8_t* dst, const Place& p, const Rows& r, const uint32_t (&w)[8]) {
+  if (p.n == kVals)
+    store32(dst + p.off, r.wide_codes, w);
+  else if (p.n)
+    *reinterpret_cast<uint4*>(dst + p.off) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 template <typename T, bool GELU, bool CKPT>
-__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const T* X, const Rows r, uint8_t* codes,
-                                                                uint8_t* scales, uint8_t* xcodes, uint8_t* xscales) {
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? kRowCtas : kRowCtas - 2)
+    quantize_fp8_kernel(const T* X, const Rows r, uint8_t* codes, uint8_t* scales, uint8_t* xcodes, uint8_t* xscales) {
   griddep_wait();
   griddep_launch_dependents();
   const Place p = place(r);
-  Piece<T> x;
-  x.zero();
-  if (p.in) x.load(X + p.off, r.wide);
-  Pairs h;
+  Piece<T, kVals> x;
+  x.load(X + p.off, p.n, r.wide);
+  Pairs<kVals> h;
   if constexpr (GELU) {
 #pragma unroll
     for (int i = 0; i < kVals / 2; ++i) h.v[i] = gelu(x.pair(i));
   }
+  uint32_t w[kVals / 4];
   if constexpr (CKPT || !GELU) {
     const uint32_t s = block_scale(x);
-    if (p.in) *reinterpret_cast<uint4*>((GELU ? xcodes : codes) + p.off) = encode16(x, inv_scale(s));
+    encode(x, inv_scale(s), w);
+    store_codes(GELU ? xcodes : codes, p, r, w);
     if (p.lead) (GELU ? xscales : scales)[p.so] = static_cast<uint8_t>(s);
   }
   if constexpr (GELU) {
     const uint32_t s = block_scale(h);
-    if (p.in) *reinterpret_cast<uint4*>(codes + p.off) = encode16(h, inv_scale(s));
+    encode(h, inv_scale(s), w);
+    store_codes(codes, p, r, w);
     if (p.lead) scales[p.so] = static_cast<uint8_t>(s);
   }
 }
 
 template <bool QUANT>
-__global__ void __launch_bounds__(kThreads) gelu_backward_fp8_kernel(const uint16_t* dH, const uint8_t* xcodes,
-                                                                     const uint8_t* xscales, const Rows r,
-                                                                     uint16_t* dX, uint8_t* codes, uint8_t* scales) {
+__global__ void __launch_bounds__(kRowThreads)
+    gelu_backward_fp8_kernel(const uint16_t* dH, const uint8_t* xcodes, const uint8_t* xscales, const Rows r,
+                             uint16_t* dX, uint8_t* codes, uint8_t* scales) {
   griddep_wait();
   griddep_launch_dependents();
   const Place p = place(r);
-  Piece<uint16_t> g;
-  g.zero();
-  if (p.in) {
-    g.load(dH + p.off, r.wide);
+  Piece<uint16_t, kVals> g;
+  g.load(dH + p.off, p.n, r.wide);
+  uint32_t w[kVals / 4] = {};
+  if (p.n == kVals) {
+    load32(xcodes + p.off, r.wide_codes, w);
+  } else if (p.n) {
     const uint4 c = *reinterpret_cast<const uint4*>(xcodes + p.off);
-    const f2 s = both(scale_value(xscales[p.so]));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < kVals / 2; ++i) {
-      const float2 v = decode2(w[i / 2] >> (16 * (i & 1)));
-      float a, b;
-      unpack(mul2(g.pair(i), gelu_slope(mul2(pack(v.x, v.y), s))), a, b);
-      const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
-      g.w[i] = *reinterpret_cast<const uint32_t*>(&o);      // the codes are those of the BF16 gradient
-    }
-    store32(dX + p.off, r.wide, g.w);
+    w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
   }
+  const f2 xs = both(p.n ? scale_value(xscales[p.so]) : 0.f);
+#pragma unroll
+  for (int i = 0; i < kVals / 2; ++i) {
+    const float2 v = decode2(w[i / 2] >> (16 * (i & 1)));
+    float a, b;
+    unpack(mul2(g.pair(i), gelu_slope(mul2(pack(v.x, v.y), xs))), a, b);
+    const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
+    g.w[i] = *reinterpret_cast<const uint32_t*>(&o);        // the codes are those of the BF16 gradient
+  }
+  if (p.n) store32(dX + p.off, r.wide, g.w);
+  if (p.n == kVals) store32(dX + p.off + 16, r.wide, g.w + 8);
   if constexpr (QUANT) {
     const uint32_t s = block_scale(g);
-    if (p.in) *reinterpret_cast<uint4*>(codes + p.off) = encode16(g, inv_scale(s));
+    encode(g, inv_scale(s), w);
+    store_codes(codes, p, r, w);
     if (p.lead) scales[p.so] = static_cast<uint8_t>(s);
   }
 }
@@ -333,22 +356,21 @@ __global__ void __launch_bounds__(kThreads) gelu_backward_fp8_kernel(const uint1
 // both the 16-byte writes (a row per 8 lanes) and the word reads of the
 // transposition (8 row groups x 4 words per warp) touch all 32 banks once.
 template <typename T, bool TRANS>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 4 : 2)
     quantize_weights_fp8_kernel(const T* W, int N, int K, int nbs, int kbs, int wide, uint8_t* codes, uint8_t* scales,
                                 uint8_t* codes_t, uint8_t* scales_t) {
-  __shared__ float wmax[2][kThreads / 32];
+  __shared__ float wmax[2][kWeightThreads / 32];
   __shared__ __align__(16) uint32_t tile[TRANS ? kBlock * kBlock / 4 : 4];
   griddep_wait();
   griddep_launch_dependents();
   const int kb = blockIdx.x % kbs, nb = blockIdx.x / kbs;
-  const int sub = threadIdx.x % kLanesPerBlock, r0 = threadIdx.x / kLanesPerBlock;
-  const int col = kb * kBlock + sub * kVals;
-  Piece<T> x[4];
+  const int sub = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int col = kb * kBlock + sub * 16;
+  Piece<T, 16> x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = nb * kBlock + r0 + 32 * i;
-    x[i].zero();
-    if (row < N && col < K) x[i].load(W + static_cast<long long>(row) * K + col, wide);
+    x[i].load(W + static_cast<long long>(row) * K + col, row < N && col < K ? 16 : 0, wide);
   }
   float m = 0.f;
 #pragma unroll 1
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     if ((threadIdx.x & 31) == 0) wmax[pass][threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[pass][i]);
+    for (int i = 0; i < kWeightThreads / 32; ++i) m = fmaxf(m, wmax[pass][i]);
     if (m != INFINITY) break;                                    // the same in every thread
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i].drop_infinities();          // as block_scale
@@ -375,7 +397,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = r0 + 32 * i, row = nb * kBlock + n;
-    const uint4 q = encode16(x[i], inv);
+    uint32_t w[4];
+    encode(x[i], inv, w);
+    const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
     if (row < N && col < K) *reinterpret_cast<uint4*>(codes + static_cast<long long>(row) * K + col) = q;
     if constexpr (TRANS) *reinterpret_cast<uint4*>(&tile[n * 32 + 4 * (sub ^ (n >> 4))]) = q;
   }
@@ -409,10 +433,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 // The next kernel of the stream may set itself up while this one runs (each
 // waits for the one before it to end before it touches memory).
 template <typename... P, typename... A>
-int launch(void (*kernel)(P...), unsigned grid, cudaStream_t st, A&&... args) {
+int launch(void (*kernel)(P...), unsigned grid, int threads, cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -424,7 +448,7 @@ int launch(void (*kernel)(P...), unsigned grid, cudaStream_t st, A&&... args) {
   return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
 }
 
-Rows make_rows(int T, int d, bool wide) {
+Rows make_rows(int T, int d, bool wide, bool wide_codes) {
   Rows r{};
   r.d = d;
   r.kbs = blocks(d);
@@ -437,6 +461,7 @@ Rows make_rows(int T, int d, bool wide) {
   r.mul = static_cast<uint32_t>(((1ull << (31 + s)) + r.kbs - 1) / r.kbs);
   r.shift = 31 + s;
   r.wide = wide;
+  r.wide_codes = wide_codes && d % 32 == 0;
   return r;
 }
 // CTAs for `total` blocks, 0 when the grid cannot hold them.
@@ -451,9 +476,10 @@ int launch_quantize(const void* X, const Rows& r, bool gelu, uint8_t* codes, uin
   const unsigned grid = grid_of(r.total);
   if (!grid) return RBQ_EINVAL;
   const T* x = static_cast<const T*>(X);
-  if (gelu && xcodes) return launch(quantize_fp8_kernel<T, true, true>, grid, st, x, r, codes, scales, xcodes, xscales);
-  if (gelu) return launch(quantize_fp8_kernel<T, true, false>, grid, st, x, r, codes, scales, xcodes, xscales);
-  return launch(quantize_fp8_kernel<T, false, false>, grid, st, x, r, codes, scales, xcodes, xscales);
+  const auto kernel = !gelu    ? quantize_fp8_kernel<T, false, false>
+                      : xcodes ? quantize_fp8_kernel<T, true, true>
+                               : quantize_fp8_kernel<T, true, false>;
+  return launch(kernel, grid, kRowThreads, st, x, r, codes, scales, xcodes, xscales);
 }
 
 template <typename T>
@@ -465,11 +491,8 @@ int launch_weights(const void* W, int N, int K, uint8_t* codes, uint8_t* scales,
   const T* w = static_cast<const T*>(W);
   const unsigned g = static_cast<unsigned>(grid);
   const int wide = aligned(W, 32);                 // rows are multiples of 32 bytes
-  if (codes_t)
-    return launch(quantize_weights_fp8_kernel<T, true>, g, st, w, N, K, nbs, kbs, wide, codes, scales, codes_t,
-                  scales_t);
-  return launch(quantize_weights_fp8_kernel<T, false>, g, st, w, N, K, nbs, kbs, wide, codes, scales, codes_t,
-                scales_t);
+  const auto kernel = codes_t ? quantize_weights_fp8_kernel<T, true> : quantize_weights_fp8_kernel<T, false>;
+  return launch(kernel, g, kWeightThreads, st, w, N, K, nbs, kbs, wide, codes, scales, codes_t, scales_t);
 }
 
 }  // namespace
@@ -486,7 +509,7 @@ extern "C" int quantize_fp8(const void* X, int dtype, int T, int d, int activati
   if (T == 0) return RBQ_OK;
   if (!X || !codes || !scales) return RBQ_EINVAL;
   if (!aligned(X, 16) || !aligned(codes, 16) || (x_codes && !aligned(x_codes, 16))) return RBQ_EALIGN;
-  const fp8::Rows r = fp8::make_rows(T, d, aligned(X, 32));          // rows are multiples of 32 bytes
+  const fp8::Rows r = fp8::make_rows(T, d, aligned(X, 32), aligned(codes, 32) && (!x_codes || aligned(x_codes, 32)));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool gelu = activation == RBQ_ACT_GELU;
   return dtype == RBQ_BF16
@@ -513,10 +536,11 @@ extern "C" int gelu_backward_fp8(const uint16_t* dH, const uint8_t* x_codes, con
   if (!dH || !x_codes || !x_scales || !dX) return RBQ_EINVAL;
   if (!aligned(dH, 16) || !aligned(x_codes, 16) || !aligned(dX, 16) || (codes && !aligned(codes, 16)))
     return RBQ_EALIGN;
-  const fp8::Rows r = fp8::make_rows(T, d, aligned(dH, 32) && aligned(dX, 32));
+  const fp8::Rows r = fp8::make_rows(T, d, aligned(dH, 32) && aligned(dX, 32),
+                                     aligned(x_codes, 32) && (!codes || aligned(codes, 32)));
   const unsigned grid = fp8::grid_of(r.total);
   if (!grid) return RBQ_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto kernel = codes ? fp8::gelu_backward_fp8_kernel<true> : fp8::gelu_backward_fp8_kernel<false>;
-  return fp8::launch(kernel, grid, st, dH, x_codes, x_scales, r, dX, codes, scales);
+  return fp8::launch(kernel, grid, fp8::kRowThreads, st, dH, x_codes, x_scales, r, dX, codes, scales);
 }
