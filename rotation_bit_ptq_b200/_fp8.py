@@ -7,6 +7,7 @@ Codes are torch.float8_e4m3fn and scales torch.float8_e8m0fnu tensors, so
 """
 
 import contextlib
+import ctypes
 
 from . import (RBQ_ACT_GELU, RBQ_ACT_NONE, RBQ_BF16, RBQ_F32, _ACTS, _check, _dtype_code, _need_cuda, _need_shape,
                check_same_device, lib)
@@ -36,11 +37,29 @@ def _on(device, stream):
             yield
 
 
-# The checks of an ordinary call cost more than its launch if each asks torch
-# for objects (devices, streams, shapes as tuples): a single token's product
-# took 15.9 us of host time that way and takes 9 us with the plain integers
-# and singletons used here.  What fails them goes through the slower checks,
-# which word the error.
+# A call on a few tokens is bound by the host.  The ordinary one -- plain
+# contiguous CUDA tensors of the right types and shapes on the current device,
+# on the current stream, with results to be allocated -- is made by _rbq_call.so
+# (csrc/rbq_call.cpp), which returns None for any other and for one that fails.  Those
+# are made here, with checks that word the error.
+_native = None
+
+
+def _ordinary():
+    """The module _rbq_call, bound to librbq.so on first use."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (loads the libraries _rbq_call.so links)
+        try:
+            from . import _rbq_call
+        except ImportError as e:
+            raise RuntimeError("_rbq_call.so is missing or does not fit this torch: build it with "
+                               "`python -m rotation_bit_ptq_b200.build`") from e
+        _rbq_call.bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
+            "quantize_fp8", "quantize_weights_fp8", "qlinear_fp8", "qlinear_fp8_wgrad", "gelu_backward_fp8")))
+        _native = _rbq_call
+    return _native
+
 
 def _operand(t, name, dtype=None):
     """A contiguous CUDA tensor, of `dtype` if one is given; returns its device's index."""
@@ -118,6 +137,10 @@ def quantize_fp8(X, activation=None, checkpoint=False, codes=None, scale=None, s
     checkpoint=True (with 'gelu') also returns the codes and scales of X
     itself, from which gelu_backward_fp8 takes the gradient: (codes, scale,
     x_codes, x_scale).  d a multiple of 16."""
+    if codes is None and scale is None and stream is None and activation in _ACTS:
+        r = (_native or _ordinary()).quantize_fp8(X, _ACTS[activation], bool(checkpoint))
+        if r is not None:
+            return r
     import torch
     dev = _matrix(X, "X")
     dtype = _dtype_code(X)
@@ -149,6 +172,10 @@ def quantize_weights_fp8(W, transposed=False, codes=None, scale=None, stream=Non
     transposed=True also returns the codes and scales of W^T, the weights of
     the layer's input gradient: (codes, scale, codes_t [K, N], scale_t).
     K a multiple of 16, and N too when transposed."""
+    if codes is None and scale is None and stream is None:
+        r = (_native or _ordinary()).quantize_weights_fp8(W, bool(transposed))
+        if r is not None:
+            return r
     import torch
     dev = _matrix(W, "W")
     dtype = _dtype_code(W)
@@ -172,6 +199,10 @@ def quantize_weights_fp8(W, transposed=False, codes=None, scale=None, stream=Non
 def qlinear_fp8(a_codes, a_scale, w_codes, w_scale, out=None, stream=None):
     """y[m, n] = sum_k (sa[m, k/128] qa[m, k]) (sw[n/128, k/128] qw[n, k]) as
     bfloat16 [M, N], on the codes of quantize_fp8 and quantize_weights_fp8."""
+    if out is None and stream is None:
+        y = (_native or _ordinary()).qlinear_fp8(a_codes, a_scale, w_codes, w_scale)
+        if y is not None:
+            return y
     import torch
     dev, M, K = _codes(a_codes, a_scale, 1, _A, torch)
     dev_w, N, K2 = _codes(w_codes, w_scale, BLOCK, _W, torch)
@@ -190,6 +221,10 @@ def qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype=None, out=None, stream=None):
     of qlinear_fp8 from the bfloat16 dY [M, N] and the codes kept of the
     layer's input; bfloat16 (the default) or float32 [N, K].  N a multiple of 8."""
     import torch
+    if out is None and stream is None and dtype in (None, torch.bfloat16, torch.float32):
+        dW = (_native or _ordinary()).qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype is torch.float32)
+        if dW is not None:
+            return dW
     dev_y = _matrix(dY, "dY", torch.bfloat16)
     dev, M, K = _codes(a_codes, a_scale, 1, _A, torch)
     T, N = dY.shape
@@ -215,6 +250,10 @@ def gelu_backward_fp8(dH, x_codes, x_scale, quantize=False, out=None, stream=Non
 
     quantize=True also returns quantize_fp8(dX), for the product that follows:
     (dX, codes, scale)."""
+    if out is None and stream is None:
+        r = (_native or _ordinary()).gelu_backward_fp8(dH, x_codes, x_scale, bool(quantize))
+        if r is not None:
+            return r
     import torch
     dev_h = _matrix(dH, "dH", torch.bfloat16)
     dev, T, d = _codes(x_codes, x_scale, 1, _X, torch)

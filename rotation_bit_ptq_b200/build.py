@@ -4,14 +4,20 @@ Run ``python -m rotation_bit_ptq_b200.build`` (or call ``build()``).  Each
 CUDA source compiles to an object under ``_build/`` (in parallel, rebuilt
 when it or a header is newer than its object), then one shared library is
 linked next to this file.  The CUDA runtime is linked statically.
+
+Beside it goes _rbq_call.so, the native part of the Python binding
+(csrc/rbq_call.cpp), compiled by the host compiler against the headers of the
+installed torch.
 """
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +30,9 @@ LIB = os.path.join(PKG, "librbq.so")
 # into the device error word instead of trapping.  Tests load it beside the
 # release library; the product path never does.
 LIB_DEBUG = os.path.join(PKG, "librbq_debug.so")
+
+# The native part of the Python binding: ordinary calls without ctypes.
+BINDING = os.path.join(PKG, "_rbq_call.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -83,7 +92,29 @@ def build(verbose=False, ptxas_info=False, jobs=None, debug=False):
             sys.stderr.write(" ".join(link) + "\n" + r.stdout + r.stderr)
         if r.returncode:
             raise RuntimeError(f"link of {os.path.basename(lib)} failed")
+    if not debug:
+        build_binding(verbose)
     return lib
+
+
+def build_binding(verbose=False):
+    """Compile csrc/rbq_call.cpp to _rbq_call.so."""
+    src = os.path.join(CSRC, "rbq_call.cpp")
+    if not _stale(BINDING, src, os.path.getmtime(os.path.join(INCLUDE, "rbq.h"))):
+        return BINDING
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda_inc, src, "-o", BINDING,
+           "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode:
+        raise RuntimeError("g++ failed on rbq_call.cpp")
+    return BINDING
 
 
 if __name__ == "__main__":
