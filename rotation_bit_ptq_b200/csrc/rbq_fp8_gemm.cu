@@ -54,7 +54,9 @@ constexpr int kThreads = 320;             // 4 epilogue warps, MMA, TMA, 4 scale
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kScaleWarp = 6;
 constexpr int kGroup = 4;                 // K slices per scale word
 constexpr int kSfBlock = 512;             // shared-memory bytes of 128 rows' scale words
-constexpr int kSfSlots = 4;               // ring of scale groups in shared memory
+constexpr int kGroups = 4;                // scale words per row and slot: the scales of up to 16 K slices
+constexpr int kSlotSlices = kGroup * kGroups;
+constexpr int kSfSlots = 2;               // ring of those slots in shared memory
 
 // Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (format 0), both
 // K-major, E8M0 scales (bit 23), N>>3 at bit 17, M>>4 at bit 24; bits 4-5 and
@@ -108,101 +110,98 @@ __device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
                : "memory");
 }
 
-// The scale bytes of a row from some K slice on, a word of four slices after
-// the other, one load each.  ALIGNED: every row is whole words.  Otherwise a row may
-// start at any address, and each of its words is put together from two
-// aligned ones, the second of which serves the next word too.  (Byte by byte,
-// the 512 x 1536 x 8960 layer, whose rows have 70 scales, took 38 us in place of 31.)
-// Loaded words may hold bytes of the rows beside it, but never of anything outside the
-// matrix of scales [lo, hi); what follows the row's last slice is not multiplied.
-template <bool ALIGNED>
+// The scales of 16 consecutive K slices of a row, four words, loaded without
+// waiting for them and put together when they are stored.  ALIGN: what the first byte's
+// address and the row's length are multiples of.  16: one load; 4: a load per
+// word; 1: the row may start at any address, and a word is put together from
+// two aligned ones.  (Byte by byte, the 512 x 1536 x 8960 layer, whose rows have 70
+// scales, took 38 us by pairs in place of 31.)  Loaded words may hold bytes of the rows beside it, but
+// never of anything outside the matrix of scales [lo, hi); what follows the
+// row's last slice is not multiplied.
+template <int ALIGN>
 struct ScaleRow {
-  // one group's word, not put together yet: whoever loads it does not wait for it
-  struct Word {
-    uint32_t word, first, shift;       // `first` counts in a row's first group only
-  };
-  const uint8_t *at, *lo, *hi;
-  uint32_t shift, first;
-  __device__ __forceinline__ void start(const uint8_t* row, const uint8_t* matrix, long long bytes) {
-    at = row;
-    if constexpr (!ALIGNED) {
-      const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
-      lo = matrix;
-      hi = matrix + bytes;
-      shift = 8u * o;
-      at = row - o;
-      first = load();
-    }
+  static constexpr int kWords = ALIGN == 1 ? kGroups + 1 : kGroups;
+  const uint8_t *row = nullptr, *lo, *hi;        // null: a row outside the matrix, all its scales 0
+  int left = 0;                                  // the row's slices from `row` on
+  uint32_t w[kWords];
+  __device__ __forceinline__ void start(const uint8_t* at, int slices, const uint8_t* matrix, long long bytes) {
+    row = at;
+    left = slices;
+    lo = matrix;
+    hi = matrix + bytes;
   }
-  __device__ __forceinline__ void none() {
-    at = lo = hi = nullptr;
-    shift = first = 0u;
-  }
-  __device__ __forceinline__ Word next() {
-    if constexpr (ALIGNED) {
-      const uint32_t w = at ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
-      at = at ? at + kGroup : at;
-      return {w, 0u, 0u};
+  __device__ __forceinline__ void none() { row = nullptr; }
+  // The next 16 slices' words.
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) w[q] = 0u;
+    if (!row) return;
+    if constexpr (ALIGN == 16) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (ALIGN == 4) {
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q)
+        if (kGroup * q < left) w[q] = __ldg(reinterpret_cast<const uint32_t*>(row) + q);
     } else {
-      return {load(), first, shift};
+      const uint8_t* p = row - offset();
+#pragma unroll
+      for (int q = 0; q < kWords; ++q, p += kGroup) {
+        if (kGroup * q >= left + static_cast<int>(offset())) break;
+        if (p >= lo && p + kGroup <= hi) {
+          w[q] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else {
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j)
+            if (p + j >= lo && p + j < hi) w[q] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+        }
+      }
     }
   }
-  // The group's scales; `carry`: the row's last word.
-  __device__ __forceinline__ static uint32_t join(const Word& w, bool first_group, uint32_t& carry) {
-    if constexpr (ALIGNED) {
-      return w.word;
-    } else {
-      const uint32_t s = __funnelshift_r(first_group ? w.first : carry, w.word, w.shift);
-      carry = w.word;
-      return s;
-    }
+  // Word q of those that were loaded.
+  __device__ __forceinline__ uint32_t word(int q) const {
+    if constexpr (ALIGN == 1) return __funnelshift_r(w[q], w[q + 1], 8u * offset());
+    return w[q];
+  }
+  __device__ __forceinline__ void step() {       // on to the 16 slices after these
+    if (row) row += kSlotSlices;
+    left -= kSlotSlices;
   }
 
  private:
-  __device__ __forceinline__ uint32_t load() {
-    const uint8_t* p = at;
-    at += kGroup;
-    if (p >= lo && p + kGroup <= hi) return __ldg(reinterpret_cast<const uint32_t*>(p));
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j)
-      if (p + j >= lo && p + j < hi) w |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
-    return w;
+  __device__ __forceinline__ uint32_t offset() const {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
   }
 };
 __device__ __forceinline__ void put_scale_word(uint8_t* block, int r, uint32_t w) {
   *reinterpret_cast<uint32_t*>(block + 16 * (r & 31) + 4 * (r >> 5)) = w;
 }
 
-enum Group { kNoGroup, kFirstGroup, kNextGroup };      // of a tile's row
-
-// One thread (row r) of the scale loaders: the words of group after group, W a
-// group, to the slots of the ring `sf`.  `fetch(w)` loads the next group's
-// words, `slot_free(slot, use)` waits until the MMAs are done with the slot's
-// last contents (false: gave up), `filled(slot)` reports.  The loads run
-// kSfSlots groups ahead, and nothing here looks at a word before its turn.
-template <int W, bool ALIGNED, typename Fetch, typename Free, typename Filled>
-__device__ __forceinline__ bool feed_scales(Fetch fetch, uint8_t* sf, int r, Free slot_free, Filled filled) {
-  typename ScaleRow<ALIGNED>::Word w[kSfSlots][W];
-  int have[kSfSlots];
-  uint32_t carry[W];
+// One thread (row r) of the scale loaders: the words of its W rows, slot after
+// slot of the ring `sf`.  `next(rows)` goes on to the next slices (false:
+// there are no more), `slot_free(slot, use)` waits until the MMAs are done with the slot's last
+// contents (false: gave up), `filled(slot)` reports.  The next slot's loads are in flight while the
+// MMAs work on the last one's.  A slot holds the scales of 16 slices: with four, each hand-over
+// (its wait acquires at cluster scope, which costs the L1 its lines) came
+// four times as often, and a slice of 128 took 760 cycles in place of ~600.
+template <int W, int ALIGN, typename Next, typename Free, typename Filled>
+__device__ __forceinline__ bool feed_scales(ScaleRow<ALIGN> (&rows)[W], Next next, uint8_t* sf, int r, Free slot_free,
+                                            Filled filled) {
+  bool more = next(rows);
+  for (uint32_t n = 0; more; ++n) {
+    const uint32_t slot = n % kSfSlots;
+    if (!slot_free(slot, n / kSfSlots)) return false;
+    uint8_t* block = sf + slot * (kGroups * W * kSfBlock);
 #pragma unroll
-  for (int i = 0; i < kSfSlots; ++i) have[i] = fetch(w[i]);
-  for (uint32_t use = 0;; ++use) {
+    for (int q = 0; q < kGroups; ++q)
 #pragma unroll
-    for (int i = 0; i < kSfSlots; ++i) {
-      if (have[i] == kNoGroup) return true;
-      if (!slot_free(i, use)) return false;
-      uint8_t* block = sf + i * W * kSfBlock;
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        put_scale_word(block + j * kSfBlock, r, ScaleRow<ALIGNED>::join(w[i][j], have[i] == kFirstGroup, carry[j]));
-      fence_proxy_async_smem();
-      __syncwarp();
-      filled(i);
-      have[i] = fetch(w[i]);
-    }
+      for (int j = 0; j < W; ++j) put_scale_word(block + (q * W + j) * kSfBlock, r, rows[j].word(q));
+    fence_proxy_async_smem();
+    __syncwarp();
+    filled(slot);
+    more = next(rows);
   }
+  return true;
 }
 
 struct Params {
@@ -212,7 +211,7 @@ struct Params {
   uint16_t* Y;
   unsigned int* err;
   int order;                  // tile order (tiles::TileOrder)
-  int sf_words;               // every part of a scale row that a CTA reads is whole words
+  int sf_align;               // 16, 4 or 1: as ScaleRow, of every part of a scale row that a CTA reads
   int y_four;                 // rows of Y 8-byte aligned
   int y_vec;                  // 2: rows of Y 32-byte aligned, 1: 16-byte aligned, 0: neither
 };
@@ -224,7 +223,8 @@ constexpr int kATile = kBM * kBK;         // 16 KB
 constexpr int kBTile = kBN / 2 * kBK;     // 16 KB: half of the tile's weight rows
 constexpr int kStage = kATile + kBTile;
 constexpr int kStages = 6;
-constexpr int kSfSlot = 3 * kSfBlock;     // 128 rows of A, 256 of B
+constexpr int kSfWord = 3 * kSfBlock;     // a scale word of 128 rows of A and 256 of B
+constexpr int kSfSlot = kGroups * kSfWord;
 // Tensor memory: accumulator 0 in columns 0..255, accumulator 1 in 224..479,
 // two buffers of scales (4 columns of A, 8 of B) from 480.
 constexpr uint32_t kAcc1 = 224, kSfCol = 480, kSfCols = 12;
@@ -234,6 +234,7 @@ struct __align__(8) Tail {
   uint64_t empty[kStages];
   uint64_t sf_full[kSfSlots];
   uint64_t sf_empty[kSfSlots];
+  uint64_t sf_used[2];           // a tensor-memory buffer of scales
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t overlap;              // the shared columns of the last tile's accumulator have been read
@@ -280,7 +281,7 @@ __device__ __forceinline__ void put_rows(uint32_t* turn, int lane, const uint32_
 }
 
 // The scale loaders of one CTA of a pair: its 128 rows of A, all 256 of B.
-template <bool ALIGNED>
+template <int ALIGN>
 __device__ __forceinline__ bool load_pair_scales(const Params& p, Tail& tl, uint8_t* sf, uint32_t rank, int tile,
                                                  int tstep) {
   const int r = threadIdx.x - 32 * kScaleWarp, lane = threadIdx.x & 31;
@@ -288,33 +289,34 @@ __device__ __forceinline__ bool load_pair_scales(const Params& p, Tail& tl, uint
   const int ntiles = ntiles_m * ntiles_n, last_nb = blocks(p.N) - 1;
   const long long sa_bytes = static_cast<long long>(p.M) * p.kbs, sw_bytes = (last_nb + 1ll) * p.kbs;
   int kb = 0;
-  ScaleRow<ALIGNED> ra, rb0, rb1;
-  // the words of the next group of K slices, of this tile or the next
-  const auto fetch = [&](typename ScaleRow<ALIGNED>::Word (&w)[3]) {
-    if (tile >= ntiles) return kNoGroup;
-    const Group which = kb == 0 ? kFirstGroup : kNextGroup;
+  ScaleRow<ALIGN> rows[3];
+  // the next slices of this tile, or the first of the next
+  const auto next = [&](ScaleRow<ALIGN> (&row)[3]) {
+    if (tile >= ntiles) return false;
     if (kb == 0) {
       int mt, nt;
       tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
       const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r, nb = nt * (kBN / kBlock);
       if (m < p.M)
-        ra.start(p.sa + static_cast<long long>(m) * p.kbs, p.sa, sa_bytes);
+        row[0].start(p.sa + static_cast<long long>(m) * p.kbs, p.kbs, p.sa, sa_bytes);
       else
-        ra.none();
-      rb0.start(p.sw + static_cast<long long>(nb) * p.kbs, p.sw, sw_bytes);
-      rb1.start(p.sw + static_cast<long long>(min(nb + 1, last_nb)) * p.kbs, p.sw, sw_bytes);
+        row[0].none();
+      row[1].start(p.sw + static_cast<long long>(nb) * p.kbs, p.kbs, p.sw, sw_bytes);
+      row[2].start(p.sw + static_cast<long long>(min(nb + 1, last_nb)) * p.kbs, p.kbs, p.sw, sw_bytes);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j) row[j].step();
     }
-    w[0] = ra.next();
-    w[1] = rb0.next();
-    w[2] = rb1.next();
-    if ((kb += kGroup) >= p.kbs) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) row[j].load();
+    if ((kb += kSlotSlices) >= p.kbs) {
       kb = 0;
       tile += tstep;
     }
-    return which;
+    return true;
   };
-  return feed_scales<3, ALIGNED>(
-      fetch, sf, r,
+  return feed_scales(
+      rows, next, sf, r,
       [&](uint32_t slot, uint32_t use) {
         return use < 1 || mbar_warp_wait(&tl.sf_empty[slot], (use - 1) & 1, &tl.abort);
       },
@@ -348,6 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tl->sf_full[s], 8);       // one arrival per loader warp of both CTAs
       mbar_init(&tl->sf_empty[s], 1);
     }
+    mbar_init(&tl->sf_used[0], 1);
+    mbar_init(&tl->sf_used[1], 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tl->acc_full[a], 1);
       mbar_init(&tl->acc_empty[a], 8);     // one arrival per epilogue warp of both CTAs
@@ -375,23 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdesc = idesc_mx(2 * kBM, kBN);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
       const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
-      uint32_t s = 0, ph = 0, it = 0, g = 0;     // operand stage, its phase; tile; scale group
+      uint32_t s = 0, ph = 0, it = 0, g = 0, n = 0;     // operand stage, its phase; tile; scale word, slot
       bool ok = true;
-      // group n's scales to tensor memory, buffer n % 2
-      const auto stage_scales = [&](uint32_t n) {
-        const uint32_t slot = n % kSfSlots;
-        // the MMAs that read the buffer's last contents (group n - 2) have completed
-        if (n >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(n - 2) % kSfSlots], ((n - 2) / kSfSlots) & 1, abort))
-          return false;
-        if (!mbar_wait_or_abort_cl(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) return false;
-        tc_fence_after();
-        const uint32_t t = tmem + kSfCol + (n & 1u) * kSfCols;
-        const uint64_t sd = sfdesc0 + ((slot * kSfSlot) >> 4);
-        cp_scales<true>(t, sd);
-        cp_scales<true>(t + 4, sd + (kSfBlock >> 4));
-        cp_scales<true>(t + 8, sd + (2 * kSfBlock >> 4));
-        return true;
-      };
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++it) {
         const uint32_t a = it & 1u, use = it >> 1;
         if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
@@ -399,8 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t acc = tmem + a * kAcc1;
         for (int ks0 = 0; ks0 < KS && ok; ks0 += kGroup, ++g) {
+          const uint32_t slot = n % kSfSlots, q = (ks0 / kGroup) % kGroups;
+          if (q == 0 && !mbar_wait_or_abort_cl(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) { ok = false; break; }
+          // the MMAs that read this buffer's last contents (word g - 2) have completed
+          if (g >= 2 && !mbar_wait_or_abort(&tl->sf_used[g & 1u], (g / 2 - 1) & 1, abort)) { ok = false; break; }
+          tc_fence_after();
           const uint32_t sfa = tmem + kSfCol + (g & 1u) * kSfCols;
-          if (!stage_scales(g)) { ok = false; break; }
+          const uint64_t sd = sfdesc0 + ((slot * kSfSlot + q * kSfWord) >> 4);
+          cp_scales<true>(sfa, sd);
+          cp_scales<true>(sfa + 4, sd + (kSfBlock >> 4));
+          cp_scales<true>(sfa + 8, sd + (2 * kSfBlock >> 4));
 #pragma unroll
           for (int j = 0; j < kGroup; ++j) {
             if (!ok || ks0 + j >= KS) break;
@@ -416,7 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_pair(&tl->empty[s], 3);
             if (++s == kStages) { s = 0; ph ^= 1u; }
           }
-          if (ok) umma_commit_pair(&tl->sf_empty[g % kSfSlots], 3);
+          if (!ok) break;
+          umma_commit_pair(&tl->sf_used[g & 1u], 1);
+          if (q == kGroups - 1 || ks0 + kGroup >= KS) {
+            umma_commit_pair(&tl->sf_empty[slot], 3);
+            ++n;
+          }
         }
         if (ok) umma_commit_pair(&tl->acc_full[a], 3);
       }
@@ -448,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kScaleWarp) {
     // ---------------- scale loaders: this CTA's 128 rows of A, all 256 of B ----------------
-    const bool ok = p.sf_words ? load_pair_scales<true>(p, *tl, sf, rank, tile0, tstep)
-                               : load_pair_scales<false>(p, *tl, sf, rank, tile0, tstep);
+    const bool ok = p.sf_align == 16  ? load_pair_scales<16>(p, *tl, sf, rank, tile0, tstep)
+                    : p.sf_align == 4 ? load_pair_scales<4>(p, *tl, sf, rank, tile0, tstep)
+                                      : load_pair_scales<1>(p, *tl, sf, rank, tile0, tstep);
     if (!ok && lane == 0) atomicOr(p.err, 32u);
   } else {
     // ---------------- epilogue ----------------
@@ -532,7 +535,8 @@ struct Few {
   static constexpr int kTTile = NT * kBK;
   static constexpr int kStage = kWTile + kTTile;
   static constexpr int kStages = (NT <= 64 ? 8 : NT == 128 ? 6 : 4);
-  static constexpr int kSfSlot = kSfBlock * (NT > 128 ? 3 : 2);
+  static constexpr int kSfWord = kSfBlock * (NT > 128 ? 3 : 2);
+  static constexpr int kSfSlot = kGroups * kSfWord;
   static constexpr uint32_t kSfCol = NT, kSfCols = NT > 128 ? 12 : 8;     // columns of a scale buffer
   static constexpr uint32_t kTmemCols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT == 64 ? 128 : NT == 128 ? 256 : 512;
   static constexpr int kRing = kStages * kStage;
@@ -546,6 +550,7 @@ struct __align__(8) FewTail {
   uint64_t empty[8];
   uint64_t sf_full[kSfSlots];
   uint64_t sf_empty[kSfSlots];
+  uint64_t sf_used[2];           // a tensor-memory buffer of scales
   uint64_t acc_full;
   uint64_t drain;
   uint32_t tmem_slot;
@@ -554,32 +559,38 @@ struct __align__(8) FewTail {
 static_assert(sizeof(FewTail) <= 512, "the tail fits");
 
 // The scale loaders of a CTA: its 128 weight rows, its NT tokens, K slices kb0 to kb1.
-template <int NT, bool ALIGNED>
+template <int NT, int ALIGN>
 __device__ __forceinline__ bool load_few_scales(const Params& p, FewTail& tl, uint8_t* sf, int nt, int m0, int kb0,
                                                 int kb1) {
-  constexpr int kWords = NT > 128 ? 3 : 2;
+  constexpr int kRows = NT > 128 ? 3 : 2;
   const int r = threadIdx.x - 32 * kScaleWarp, lane = threadIdx.x & 31;
-  ScaleRow<ALIGNED> row[kWords];
-  row[0].start(p.sw + static_cast<long long>(nt) * p.kbs + kb0, p.sw, static_cast<long long>(blocks(p.N)) * p.kbs);
-#pragma unroll
-  for (int j = 1; j < kWords; ++j) {
-    const int t = r + 128 * (j - 1);
-    if (t < NT && m0 + t < p.M)
-      row[j].start(p.sa + static_cast<long long>(m0 + t) * p.kbs + kb0, p.sa, static_cast<long long>(p.M) * p.kbs);
-    else
-      row[j].none();
-  }
+  ScaleRow<ALIGN> rows[kRows];
   int kb = kb0;
-  const auto fetch = [&](typename ScaleRow<ALIGNED>::Word (&w)[kWords]) {
-    if (kb >= kb1) return kNoGroup;
-    const Group which = kb == kb0 ? kFirstGroup : kNextGroup;
+  const auto next = [&](ScaleRow<ALIGN> (&row)[kRows]) {
+    if (kb >= kb1) return false;
+    if (kb == kb0) {
+      row[0].start(p.sw + static_cast<long long>(nt) * p.kbs + kb0, p.kbs - kb0, p.sw,
+                   static_cast<long long>(blocks(p.N)) * p.kbs);
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = row[j].next();
-    kb += kGroup;
-    return which;
+      for (int j = 1; j < kRows; ++j) {
+        const int t = r + 128 * (j - 1);
+        if (t < NT && m0 + t < p.M)
+          row[j].start(p.sa + static_cast<long long>(m0 + t) * p.kbs + kb0, p.kbs - kb0, p.sa,
+                       static_cast<long long>(p.M) * p.kbs);
+        else
+          row[j].none();
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) row[j].step();
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) row[j].load();
+    kb += kSlotSlices;
+    return true;
   };
-  return feed_scales<kWords, ALIGNED>(
-      fetch, sf, r,
+  return feed_scales(
+      rows, next, sf, r,
       [&](uint32_t slot, uint32_t use) {
         return use < 1 || mbar_warp_wait(&tl.sf_empty[slot], (use - 1) & 1, &tl.abort);
       },
@@ -661,6 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tl->sf_full[s], 4);
       mbar_init(&tl->sf_empty[s], 1);
     }
+    mbar_init(&tl->sf_used[0], 1);
+    mbar_init(&tl->sf_used[1], 1);
     mbar_init(&tl->acc_full, 1);
     mbar_init(&tl->drain, 1);
     tl->abort = 0u;
@@ -686,15 +699,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s = 0, ph = 0, g = 0;
       bool ok = true;
       for (int kg = kb0; kg < kb1 && ok; kg += kGroup, ++g) {
-        const uint32_t slot = g % kSfSlots;
-        if (g >= 2 && !mbar_wait_or_abort(&tl->sf_empty[(g - 2) % kSfSlots], ((g - 2) / kSfSlots) & 1, abort)) {
-          ok = false;
-          break;
-        }
-        if (!mbar_wait_or_abort(&tl->sf_full[slot], (g / kSfSlots) & 1, abort)) { ok = false; break; }
+        const uint32_t q = g % kGroups, n = g / kGroups, slot = n % kSfSlots;
+        if (q == 0 && !mbar_wait_or_abort(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) { ok = false; break; }
+        if (g >= 2 && !mbar_wait_or_abort(&tl->sf_used[g & 1u], (g / 2 - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t sfa = tmem + F::kSfCol + (g & 1u) * F::kSfCols;
-        const uint64_t sd = sfdesc0 + ((slot * F::kSfSlot) >> 4);
+        const uint64_t sd = sfdesc0 + ((slot * F::kSfSlot + q * F::kSfWord) >> 4);
         cp_scales<false>(sfa, sd);
         cp_scales<false>(sfa + 4, sd + (kSfBlock >> 4));
         if constexpr (NT > 128) cp_scales<false>(sfa + 8, sd + (2 * kSfBlock >> 4));
@@ -713,7 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&tl->empty[s]);
           if (++s == kS) { s = 0; ph ^= 1u; }
         }
-        if (ok) umma_commit(&tl->sf_empty[slot]);
+        if (!ok) break;
+        umma_commit(&tl->sf_used[g & 1u]);
+        if (q == kGroups - 1) umma_commit(&tl->sf_empty[slot]);
       }
       if (ok)
         umma_commit(&tl->acc_full);
@@ -737,8 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) atomicOr(p.err, 16u);
     }
   } else if (warp >= kScaleWarp) {
-    const bool ok = p.sf_words ? load_few_scales<NT, true>(p, *tl, sf, nt, m0, kb0, kb1)
-                               : load_few_scales<NT, false>(p, *tl, sf, nt, m0, kb0, kb1);
+    const bool ok = p.sf_align == 16  ? load_few_scales<NT, 16>(p, *tl, sf, nt, m0, kb0, kb1)
+                    : p.sf_align == 4 ? load_few_scales<NT, 4>(p, *tl, sf, nt, m0, kb0, kb1)
+                                      : load_few_scales<NT, 1>(p, *tl, sf, nt, m0, kb0, kb1);
     if (!ok && lane == 0) atomicOr(p.err, 32u);
   } else {
     // partial sums -> red[token][128 columns] where the operands were: every
@@ -955,7 +968,9 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
   p.sa = a_scales;
   p.sw = w_scales;
   p.Y = Y;
-  p.sf_words = p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4);
+  p.sf_align = p.kbs % 16 == 0 && aligned(a_scales, 16) && aligned(w_scales, 16) ? 16
+               : p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4)  ? 4
+                                                                                  : 1;
   p.y_four = N % 4 == 0 && aligned(Y, 8);
   p.y_vec = N % 16 == 0 && aligned(Y, 32) ? 2 : N % 8 == 0 && aligned(Y, 16) ? 1 : 0;
   int rc = device_error_word_ptr(&p.err);
@@ -968,7 +983,8 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const fp8::Plan plan = fp8::make_plan(M, N, p.kbs, sms);
   const int S = plan.S;
-  for (int r = 1; r < S; ++r) p.sf_words = p.sf_words && static_cast<long long>(p.kbs) * r / S % 4 == 0;
+  for (int r = 1; r < S; ++r)
+    while (static_cast<long long>(p.kbs) * r / S % p.sf_align) p.sf_align = p.sf_align == 16 ? 4 : 1;
   switch (plan.NT) {
     case 16: return fp8::launch_few<16>(a_codes, w_codes, p, S, dev, st);
     case 32: return fp8::launch_few<32>(a_codes, w_codes, p, S, dev, st);
