@@ -37,6 +37,9 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "rbq_fp8.cuh"
 #include "rbq_internal.h"
 #include "rbq_qcodes.cuh"
@@ -911,33 +914,35 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 }
 
 // Which kernel, with how many tokens to a tile and how many CTAs to a tile's
-// K: what takes least by a linear model, in ns, of the times of 24 layers of 1 to
-// 4096 tokens, 64 to 16384 outputs and 256 to 16384 inputs with every choice
-// of both (its choice was the best or within 6 % of it in all of them):
-//   a launch `start[NT]`, a K slice `slice[NT]`, each further wave of CTAs `wave`, a
+// K: what takes least by a linear model, in ns, of the times of 35 layers of 1
+// to 32760 tokens, 64 to 16384 outputs and 256 to 16384 inputs with every
+// choice of both (its choice was the best or within 6 % of it in all of them):
+//   a launch `start`, each K slice of a wave of CTAs `slice` or what 17 TB/s take
+//   from L2 for all of them, each further wave 5000 (2400 by pairs), a
 //   cluster's joint sum 600 + 200 S + 8 NT.
 // Few tokens to a tile fill the GPU and share little; the pair kernel shares
-// most and pays from about 100 tiles of 256 x 256.  For instance 512 x 4096 x
-// 4096: 17.4 us by pairs, 11.1 with NT = 128 (S = 1), 13.3 with NT = 256 and S = 2; 1 x 4096 x
-// 4096: 5.3 us with S = 4, 6.7 with S = 1; 4096 x 4096 x 4096: 57.6 us by pairs, 65.4 with
-// NT = 256; 333 x 1001 x 1552: 5.9 us with NT = 32, 13.7 by pairs.
+// most and pays from about 75 tiles of 256 x 256.  For instance 512 x 4096 x
+// 4096: 16.8 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and S = 2;
+// 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096: 56.1 us by
+// pairs, 66.0 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32, 13.6 by pairs.
 struct Plan {
   int NT, S;                // tokens to a tile (0: the pair kernel), CTAs to a cluster
 };
 Plan make_plan(int M, int N, int kbs, int sms) {
-  const auto waves = [](long long tiles, int n) { return (tiles + n - 1) / n; };
-  const long long pair_waves = waves(((M + 255LL) / 256) * ((N + 255LL) / 256), sms / 2);
+  const auto up = [](double a, double b) { return std::ceil(a / b); };
+  const double pair_waves = up(up(M, 256) * up(N, 256), sms / 2);
   Plan best{0, 1};
-  long long least = 6700 + 1900 * (pair_waves - 1) + 340 * pair_waves * kbs;
+  double least = 6500 + 2400 * (pair_waves - 1) + 328 * pair_waves * kbs;
   constexpr struct {
     int NT, start, slice;
-  } kinds[] = {{16, 2300, 150}, {32, 2750, 150}, {64, 2750, 190}, {128, 3300, 212}, {256, 6900, 270}};
+  } kinds[] = {{16, 2350, 145}, {32, 2850, 145}, {64, 2950, 180}, {128, 3250, 218}, {256, 6200, 289}};
   for (const auto& k : kinds) {
-    const long long tiles = static_cast<long long>(blocks(N)) * ((M + k.NT - 1LL) / k.NT);
+    const double tiles = up(N, 128) * up(M, k.NT);
+    const double l2 = tiles * kbs * ((kBM + k.NT) * kBK) / 17000;
     for (int S = 1; S <= 8 && S <= kbs; S *= 2) {
-      const long long w = waves(tiles * S, sms);
-      const long long t = k.start + 5000 * (w - 1) + w * ((kbs + S - 1) / S) * k.slice +
-                          (S > 1 ? 600 + 200 * S + 8 * k.NT : 0);
+      const double waves = up(tiles * S, sms);
+      const double t = k.start + 5000 * (waves - 1) + std::max(waves * up(kbs, S) * k.slice, l2) +
+                       (S > 1 ? 600 + 200 * S + 8 * k.NT : 0);
       if (t < least) {
         least = t;
         best = {k.NT, S};

@@ -136,10 +136,12 @@ def test_quantize_edge_values(dtype):
 
 
 def test_decoded_values_are_exact_in_bf16():
+    """(exp(25 z) is infinite for z > 3.55, which one run in 80 draws: such a
+    value's code is NaN, and NaN is compared as equal to itself.)"""
     x = torch.randn(64, 512, device="cuda") * torch.exp(torch.randn(64, 1, device="cuda") * 25)
     q, s = rbq.quantize_fp8(x.contiguous())
     v = q.float() * s.float().repeat_interleave(128, 1)
-    assert torch.equal(v, v.bfloat16().float())
+    assert torch.allclose(v, v.bfloat16().float(), rtol=0, atol=0, equal_nan=True)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -377,13 +379,20 @@ def test_more_than_2_31_elements():
     del x
     w, ws = rbq.quantize_weights_fp8(torch.randn(128, d, device="cuda"))
     y = rbq.qlinear_fp8(q, s, w, ws)
-    assert torch.equal(y[-3:], rbq.qlinear_fp8(q[-259:].contiguous(), s[-259:].contiguous(), w, ws)[-3:])
+    # both against the 64-bit values: layers of 140000 and of 259 tokens add
+    # their products in different orders (the latter splits K), so that their
+    # fp32 sums, each within the bound of the exact one, need not be equal
+    a, b = _held(q[-3:], s[-3:]), _held(w, ws, 128)
+    for rows in (y[-3:], rbq.qlinear_fp8(q[-259:].contiguous(), s[-259:].contiguous(), w, ws)[-3:]):
+        _close(bf16_to_numpy(rows), a @ b.T, np.abs(a) @ np.abs(b).T, d / 32)
     assert not y[:-3].any()
     del q, s, y
     a, asc = rbq.quantize_fp8(torch.randn(70000, 16, device="cuda"))
     w, ws = rbq.quantize_weights_fp8(torch.randn(32768, 16, device="cuda"))
     y = rbq.qlinear_fp8(a, asc, w, ws)
-    assert torch.equal(y[-2:], rbq.qlinear_fp8(a[-300:].contiguous(), asc[-300:].contiguous(), w, ws)[-2:])
+    av, wv = _held(a[-2:], asc[-2:]), _held(w, ws, 128)
+    for rows in (y[-2:], rbq.qlinear_fp8(a[-300:].contiguous(), asc[-300:].contiguous(), w, ws)[-2:]):
+        _close(bf16_to_numpy(rows), av @ wv.T, np.abs(av) @ np.abs(wv).T, 1)
 
 
 # ---- streams, graphs, repeated calls ---------------------------------------------------------
