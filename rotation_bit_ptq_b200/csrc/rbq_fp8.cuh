@@ -22,6 +22,8 @@
 
 #include <cstdint>
 
+#include "rbq_sm100.cuh"
+
 namespace rbq {
 namespace fp8 {
 
@@ -64,8 +66,8 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
 // True in one thread of a converged warp, the one that issues its MMAs or its
 // TMA copies.  The operands of both are uniform registers: under a test of the
 // lane number the compiler moves each of them there by a loop over the threads
-// that might be active (173 cycles a tcgen05.mma; a 256 x 256 x 32 one runs for 128), under
-// elect.sync it knows that there is one.
+// that might be active (173 cycles a tcgen05.mma; a 256 x 256 x 32 one runs for
+// 128), under elect.sync it knows that there is one.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -74,6 +76,29 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0u;
+}
+// Arrive on an mbarrier of any CTA of the cluster, ordering nothing but the
+// execution: for a warp that has read tensor memory (tcgen05.wait::ld and
+// tcgen05.fence::before_thread_sync order those reads) and hands its columns back.
+// A releasing arrival would also wait for the warp's stores to global memory.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// A box of a tensor map from shared to global memory (what lies outside the
+// tensor is left out), as a bulk group of its own.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(static_cast<uint32_t>(__cvta_generic_to_shared(src)))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's bulk groups have read their shared memory / have been written.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// As mbar_warp_wait, for a barrier that threads of the other CTA arrive on.
+__device__ __forceinline__ bool mbar_warp_wait_cl(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  return !__any_sync(0xffffffffu, !sm100::mbar_wait_or_abort_cl(bar, parity, abort));
 }
 // The warp's number, in a form that the compiler knows to be the same in all its threads.
 __device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }

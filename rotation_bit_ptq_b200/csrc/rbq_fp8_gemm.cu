@@ -106,21 +106,15 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
          (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
 }
 
-// 32 bytes (eight words) to global memory in one store; dst 32-byte aligned.
-__device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // The scales of 16 consecutive K slices of a row, four words, loaded without
-// waiting for them and put together when they are stored.  ALIGN: what the first byte's
-// address and the row's length are multiples of.  16: one load; 4: a load per
-// word; 1: the row may start at any address, and a word is put together from
-// two aligned ones.  (Byte by byte, the 512 x 1536 x 8960 layer, whose rows have 70
-// scales, took 38 us by pairs in place of 31.)  Loaded words may hold bytes of the rows beside it, but
-// never of anything outside the matrix of scales [lo, hi); what follows the
-// row's last slice is not multiplied.
+// waiting for them and put together when they are stored.  ALIGN: what the
+// first byte's address and the row's length are multiples of.  16: one load; 4:
+// a load per word; 1: the row may start at any address, and a word is put
+// together from two aligned ones.  (Byte by byte, the 512 x 1536 x 8960 layer,
+// whose rows have 70 scales, took 38 us by pairs in place of 31.)  Loaded words
+// may hold bytes of the rows beside it, but never of anything outside the
+// matrix of scales [lo, hi); what follows the row's last slice is not
+// multiplied.
 template <int ALIGN>
 struct ScaleRow {
   static constexpr int kWords = ALIGN == 1 ? kGroups + 1 : kGroups;
@@ -181,12 +175,13 @@ __device__ __forceinline__ void put_scale_word(uint8_t* block, int r, uint32_t w
 }
 
 // One thread (row r) of the scale loaders: the words of its W rows, slot after
-// slot of the ring `sf`.  `next(rows)` goes on to the next slices (false:
-// there are no more), `slot_free(slot, use)` waits until the MMAs are done with the slot's last
-// contents (false: gave up), `filled(slot)` reports.  The next slot's loads are in flight while the
-// MMAs work on the last one's.  A slot holds the scales of 16 slices: with four, each hand-over
-// (its wait acquires at cluster scope, which costs the L1 its lines) came
-// four times as often, and a slice of 128 took 760 cycles in place of ~600.
+// slot of the ring `sf`.  `next(rows)` goes on to the next slices (false: there
+// are no more), `slot_free(slot, use)` waits until the MMAs are done with the
+// slot's last contents (false: gave up), `filled(slot)` reports.  The next
+// slot's loads are in flight while the MMAs work on the last one's.  A slot
+// holds the scales of 16 slices: with four, each hand-over (its wait acquires
+// at cluster scope, which costs the L1 its lines) came four times as often, and
+// a slice of 128 took 760 cycles in place of ~600.
 template <int W, int ALIGN, typename Next, typename Free, typename Filled>
 __device__ __forceinline__ bool feed_scales(ScaleRow<ALIGN> (&rows)[W], Next next, uint8_t* sf, int r, Free slot_free,
                                             Filled filled) {
@@ -216,7 +211,7 @@ struct Params {
   int order;                  // tile order (tiles::TileOrder)
   int sf_align;               // 16, 4 or 1: as ScaleRow, of every part of a scale row that a CTA reads
   int y_four;                 // rows of Y 8-byte aligned
-  int y_vec;                  // 2: rows of Y 32-byte aligned, 1: 16-byte aligned, 0: neither
+  int y_tma;                  // rows of Y 16-byte aligned: they go out by TMA
 };
 
 // ---- many tokens --------------------------------------------------------------
@@ -246,39 +241,52 @@ struct __align__(8) Tail {
   volatile uint32_t abort;
 };
 
-constexpr int kTurn = 32 * 17;            // words a warp turns a 32 x 32 piece of the output in
-constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + 4 * 4 * kTurn + sizeof(Tail) + 64;
+constexpr int kPiece = 32 * 128;          // bytes of a warp's 32 rows x 64 columns of the output
+constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + 4 * kPiece + sizeof(Tail) + 64;
+static_assert(kSfSlots * kSfSlot % 1024 == 0, "pieces are swizzle atoms");
 
-// A warp's 32 rows x 32 columns of the output (row m0 + lane in each lane, 16
-// words of two BF16) to rows whose length or address allows no vectors (an odd
-// N, the right edge).  Through shared memory, rows of 17 words, so that 16 lanes write
-// one row with 4-byte stores: row by lane, each 2-byte store of the warp falls
-// into 32 sectors (a 333 x 1001 x 1552 layer took 44 us).  Where a row begins in
-// the middle of a word, its words are put together from two neighbours and
-// its two ends go out as halves.
-__device__ __forceinline__ void put_rows(uint32_t* turn, int lane, const uint32_t (&o)[16], const Params& p, int m0,
+__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's 32 rows x 64 columns of the output (row m0 + lane in each lane, 32
+// words of two BF16) to rows whose length or address TMA does not take (N no
+// multiple of 8).  Row by lane, each 2-byte store of the warp falls into 32
+// sectors (a 333 x 1001 x 1552 layer took 44 us by pairs in place of 14), so the
+// rows go through shared memory, word j of row r at j ^ r, and the warp writes
+// one after the other with 4-byte stores.  A row that begins in the middle of a
+// word is shifted by a half while it is still in its lane's registers; the lane writes
+// the halves that are left at its ends.  One warp of the scheduler does all
+// this, a few cycles an instruction: what counts is how many a row takes.
+__device__ __forceinline__ void put_rows(uint32_t* turn, int lane, const uint32_t (&o)[32], const Params& p, int m0,
                                          int nb) {
+  const int rows = min(32, p.M - m0), cols = min(64, p.N - nb);
+  uint16_t* first = p.Y + static_cast<long long>(m0) * p.N + nb;      // of row 0
+  const auto half_of = [&](int r) {                // row r begins in the middle of a word
+    return static_cast<int>((reinterpret_cast<uintptr_t>(first) >> 1) + static_cast<uintptr_t>(r) * p.N) & 1;
+  };
+  const int h = half_of(lane);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) turn[17 * lane + j] = o[j];
-  __syncwarp();
-  const int l = lane & 15, cols = min(32, p.N - nb);
-  uint32_t w[16], next[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t* row = turn + 17 * (2 * i + (lane >> 4));
-    w[i] = row[l];
-    next[i] = row[min(l + 1, 15)];
+  for (int j = 0; j < 32; ++j)
+    turn[32 * lane + (j ^ lane)] = __byte_perm(o[j], o[min(j + 1, 31)], h ? 0x5432u : 0x3210u);
+  if (lane < rows) {
+    uint16_t* row = first + static_cast<long long>(lane) * p.N;
+    const int words = (cols - h) >> 1;
+    if (h) row[0] = static_cast<uint16_t>(o[0]);
+    if ((cols - h) & 1) row[cols - 1] = static_cast<uint16_t>(turn[32 * lane + (words ^ lane)]);
   }
-  uint16_t* dst = p.Y + static_cast<long long>(m0 + (lane >> 4)) * p.N + nb + 2 * l;
-  const int rows = p.M - m0 - (lane >> 4);
+  __syncwarp();
+  // rows r and r + 1 alternate between two alignments (or share one)
+  const int h0 = half_of(0), h1 = half_of(1);
+  uint32_t* even = reinterpret_cast<uint32_t*>(first + h0) + lane;
+  uint32_t* odd = reinterpret_cast<uint32_t*>(first + p.N + h1) + lane;
+  const bool in0 = lane < (cols - h0) >> 1, in1 = lane < (cols - h1) >> 1;
 #pragma unroll
-  for (int i = 0; i < 16; ++i, dst += 2 * static_cast<long long>(p.N)) {
-    const int odd = (reinterpret_cast<uintptr_t>(dst) & 2u) != 0;      // the row begins in the middle of a word
-    const bool in = 2 * i < rows;
-    const bool whole = 2 * l + odd + 1 < cols;                         // never for l = 15 when odd
-    if (in && whole) *reinterpret_cast<uint32_t*>(dst + odd) = odd ? __byte_perm(w[i], next[i], 0x5432) : w[i];
-    if (in && !whole && 2 * l + odd < cols) dst[odd] = static_cast<uint16_t>(odd ? w[i] >> 16 : w[i]);
-    if (in && odd && l == 0) dst[0] = static_cast<uint16_t>(w[i]);
+  for (int r = 0; r < 32; r += 2, even += p.N, odd += p.N) {        // two rows on: 2 N halves
+    const uint32_t a = turn[32 * r + (lane ^ r)], b = turn[32 * (r + 1) + (lane ^ (r + 1))];
+    if (in0 && r < rows) *even = a;
+    if (in1 && r + 1 < rows) *odd = b;
   }
   __syncwarp();
 }
@@ -329,15 +337,17 @@ __device__ __forceinline__ bool load_pair_scales(const Params& p, Tail& tl, uint
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmY, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* sf = ops + kStages * kStage;
-  Tail* tl = reinterpret_cast<Tail*>(sf + kSfSlots * kSfSlot + 4 * 4 * kTurn);
+  Tail* tl = reinterpret_cast<Tail*>(sf + kSfSlots * kSfSlot + 4 * kPiece);
   const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int tile0 = static_cast<int>(cluster_id_x()), tstep = static_cast<int>(cluster_count_x());
+  // clusters are pairs of neighbouring blocks; the compiler knows that these are the same in all threads
+  const uint32_t rank = blockIdx.x & 1u;
+  const int tile0 = static_cast<int>(blockIdx.x >> 1), tstep = static_cast<int>(gridDim.x >> 1);
   const int ntiles_m = (p.M + 2 * kBM - 1) / (2 * kBM), ntiles_n = (p.N + kBN - 1) / kBN;
   const int ntiles = ntiles_m * ntiles_n;
   const int KS = p.kbs;
@@ -371,14 +381,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();                          // a pair's barriers are signalled from both CTAs
   tc_fence_after();
-  const uint32_t tmem = tl->tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tl->tmem_slot, 0);
   griddep_wait();
   griddep_launch_dependents();
 
   if (warp == kMmaWarp) {
     // ---------------- MMA issuer (the even CTA's) ----------------
-    if (rank == 0 && elect_one()) {
-      issuer = true;
+    // The warp goes through the loop together and one thread issues, so that
+    // everything an MMA takes is uniform to the compiler.  With one thread in the whole loop it moved
+    // values from register to register for each MMA, more or fewer of them with every change to the kernel: 532 to
+    // 620 cycles a slice.  (fp8_few_kernel's loop is short, and the joint waits cost it more: 5.2 us in place of 4.9
+    // for 1 x 4096 x 4096.)
+    if (rank == 0) {
       constexpr uint32_t kIdesc = idesc_mx(2 * kBM, kBN);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
       const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf));
@@ -386,46 +400,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++it) {
         const uint32_t a = it & 1u, use = it >> 1;
-        if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
-        if (it >= 1 && !mbar_wait_or_abort_cl(&tl->overlap, (it - 1) & 1, abort)) { ok = false; break; }
+        if (use >= 1 && !mbar_warp_wait_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
+        if (it >= 1 && !mbar_warp_wait_cl(&tl->overlap, (it - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t acc = tmem + a * kAcc1;
         for (int ks0 = 0; ks0 < KS && ok; ks0 += kGroup, ++g) {
           const uint32_t slot = n % kSfSlots, q = (ks0 / kGroup) % kGroups;
-          if (q == 0 && !mbar_wait_or_abort_cl(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) { ok = false; break; }
+          if (q == 0 && !mbar_warp_wait_cl(&tl->sf_full[slot], (n / kSfSlots) & 1, abort)) { ok = false; break; }
           // the MMAs that read this buffer's last contents (word g - 2) have completed
-          if (g >= 2 && !mbar_wait_or_abort(&tl->sf_used[g & 1u], (g / 2 - 1) & 1, abort)) { ok = false; break; }
+          if (g >= 2 && !mbar_warp_wait(&tl->sf_used[g & 1u], (g / 2 - 1) & 1, abort)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sfa = tmem + kSfCol + (g & 1u) * kSfCols;
           const uint64_t sd = sfdesc0 + ((slot * kSfSlot + q * kSfWord) >> 4);
-          cp_scales<true>(sfa, sd);
-          cp_scales<true>(sfa + 4, sd + (kSfBlock >> 4));
-          cp_scales<true>(sfa + 8, sd + (2 * kSfBlock >> 4));
+          if (elect_one()) {
+            cp_scales<true>(sfa, sd);
+            cp_scales<true>(sfa + 4, sd + (kSfBlock >> 4));
+            cp_scales<true>(sfa + 8, sd + (2 * kSfBlock >> 4));
+          }
 #pragma unroll
           for (int j = 0; j < kGroup; ++j) {
             if (!ok || ks0 + j >= KS) break;
-            if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+            if (!mbar_warp_wait(&tl->full[s], ph, abort)) { ok = false; break; }
             tc_fence_after();
             const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kStage)) >> 4);
             const uint64_t bd = ad + (kATile >> 4);
-            const uint32_t id = kIdesc | idesc_byte(j);
-            umma_mx<true>(acc, ad, bd, id, sfa, sfa + 4, j != 0 || ks0 != 0);
-            umma_mx<true>(acc, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);     // +32 bytes = 32 values of K
-            umma_mx<true>(acc, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
-            umma_mx<true>(acc, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
-            umma_commit_pair(&tl->empty[s], 3);
+            const uint32_t id = kIdesc | idesc_byte(j), add = j != 0 || ks0 != 0;
+            if (elect_one()) {
+              umma_mx<true>(acc, ad, bd, id, sfa, sfa + 4, add);
+              umma_mx<true>(acc, ad + 2, bd + 2, id, sfa, sfa + 4, 1u);     // +32 bytes = 32 values of K
+              umma_mx<true>(acc, ad + 4, bd + 4, id, sfa, sfa + 4, 1u);
+              umma_mx<true>(acc, ad + 6, bd + 6, id, sfa, sfa + 4, 1u);
+              umma_commit_pair(&tl->empty[s], 3);
+            }
             if (++s == kStages) { s = 0; ph ^= 1u; }
           }
           if (!ok) break;
-          umma_commit_pair(&tl->sf_used[g & 1u], 1);
-          if (q == kGroups - 1 || ks0 + kGroup >= KS) {
-            umma_commit_pair(&tl->sf_empty[slot], 3);
-            ++n;
+          const bool last = q == kGroups - 1 || ks0 + kGroup >= KS;
+          if (elect_one()) {
+            umma_commit_pair(&tl->sf_used[g & 1u], 1);
+            if (last) umma_commit_pair(&tl->sf_empty[slot], 3);
           }
+          if (last) ++n;
         }
-        if (ok) umma_commit_pair(&tl->acc_full[a], 3);
+        if (ok && elect_one()) umma_commit_pair(&tl->acc_full[a], 3);
       }
-      if (!ok) atomicOr(p.err, 2u);
+      if (!ok && lane == 0) atomicOr(p.err, 2u);
+      issuer = elect_one();
     }
   } else if (warp == kTmaWarp) {
     // ---------------- TMA producer: each CTA its own rows, both CTAs' bytes on the even CTA's barrier ----------------
@@ -459,59 +479,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, 32u);
   } else {
     // ---------------- epilogue ----------------
-    const int r = 32 * warp + lane;         // row within this CTA's 128 rows of the tile
-    uint32_t* turn = reinterpret_cast<uint32_t*>(sf + kSfSlots * kSfSlot) + warp * kTurn;
+    uint8_t* piece = sf + kSfSlots * kSfSlot + warp * kPiece;
     uint32_t it = 0;
     for (int tile = tile0; tile < ntiles; tile += tstep, ++it) {
       const uint32_t a = it & 1u, use = it >> 1;
+      int mt, nt;                             // before the wait: the next tile's MMAs wait for what follows it
+      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
       if (!mbar_warp_wait(&tl->acc_full[a], use & 1, abort)) {   // warp-uniform: tmem loads follow
         if (lane == 0) atomicOr(p.err, 4u);
         break;
       }
       tc_fence_after();
-      int mt, nt;
-      tiles::tile_coords(tile, ntiles_m, ntiles_n, p.order, mt, nt);
-      const int m = mt * 2 * kBM + static_cast<int>(rank) * kBM + r;
+      const int m0 = mt * 2 * kBM + static_cast<int>(rank) * kBM + 32 * warp;     // this warp's rows
       const uint32_t tq = tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * kAcc1;
 #pragma unroll 1
-      for (int c = 0; c < kBN / 32; ++c) {
-        const int cc = a == 0 ? kBN / 32 - 1 - c : c;   // the columns both accumulators share come first
-        uint32_t v[32];
-        tmem_ld32(tq + 32 * cc, v);
-        tmem_wait_ld();
-        if (c == 0) {
-          tc_fence_before();
+      for (int c = 0; c < kBN / 64; ++c) {
+        const int cc = a == 0 ? kBN / 64 - 1 - c : c;   // the columns both accumulators share come first
+        uint32_t o[32];
+        {
+          uint32_t u[32], v[32];
+          tmem_ld32(tq + 64 * cc, u);
+          tmem_ld32(tq + 64 * cc + 32, v);
+          tmem_wait_ld();
+          if (c == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(mapa_shared(&tl->overlap, 0));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            o[j] = bf16x2(u[2 * j], u[2 * j + 1]);
+            o[16 + j] = bf16x2(v[2 * j], v[2 * j + 1]);
+          }
+        }
+        const int nb = nt * kBN + 64 * cc;
+        if (m0 >= p.M || nb >= p.N) continue;           // the same in the whole warp
+        if (p.y_tma) {
+          if (lane == 0) bulk_wait_read();              // the last piece has left
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->overlap, 0));
-        }
-        const int nb = nt * kBN + 32 * cc;
-        if (m - lane >= p.M || nb >= p.N) continue;       // the same in the whole warp
-        uint16_t* dst = p.Y + static_cast<long long>(m) * p.N + nb;
-        uint32_t o[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-          o[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        if (nb + 32 <= p.N && p.y_vec == 2) {
-          if (m < p.M) {
-            st_v8(dst, o);
-            st_v8(dst + 16, o + 8);
-          }
-        } else if (nb + 32 <= p.N && p.y_vec == 1) {
-          if (m < p.M) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(piece + sw128_offset(lane, j)) =
+                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tmY, nb, m0, piece);
         } else {
-          put_rows(turn, lane, o, p, m - lane, nb);
+          put_rows(reinterpret_cast<uint32_t*>(piece), lane, o, p, m0, nb);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->acc_empty[a], 0));
+      if (lane == 0) mbar_arrive_relaxed(mapa_shared(&tl->acc_empty[a], 0));
     }
+    if (lane == 0) bulk_wait();
   }
 
   tc_fence_before();
@@ -806,6 +827,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (S > 1) cluster_sync();       // no CTA leaves while another reads its sums
 }
 
+// BF16 [M, N], boxes of 32 rows x 64 columns, 128B swizzle.
+int encode_out_map(CUtensorMap* map, uint16_t* base, int M, int N) {
+  auto fn = qfast::encode_fn();
+  if (!fn) return RBQ_ECUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+  const cuuint64_t strides[1] = {2 * static_cast<cuuint64_t>(N)};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
+}
+
 // uint8 [rows, K] K-major, boxes of box_rows x 128 bytes, 128B swizzle.
 int encode_map(CUtensorMap* map, const uint8_t* base, int rows, int K, int box_rows) {
   auto fn = qfast::encode_fn();
@@ -864,8 +899,10 @@ int launch_pair(const uint8_t* a, const uint8_t* w, Params p, int dev, cudaStrea
   int clusters = pair_clusters(dev);
   if (clusters < 1) return RBQ_ECUDA;
   p.order = tiles::tile_order(dev, 1LL * p.M * p.K, 1LL * p.N * p.K);
-  CUtensorMap mA, mB;
-  int rc = encode_map(&mA, a, p.M, p.K, kBM);
+  CUtensorMap mA, mB, mY{};
+  int rc = p.y_tma ? encode_out_map(&mY, p.Y, p.M, p.N) : RBQ_OK;
+  if (rc != RBQ_OK) return rc;
+  rc = encode_map(&mA, a, p.M, p.K, kBM);
   if (rc != RBQ_OK) return rc;
   if ((rc = encode_map(&mB, w, p.N, p.K, kBN / 2)) != RBQ_OK) return rc;
   const long long ntiles = ((p.M + 2LL * kBM - 1) / (2 * kBM)) * ((p.N + kBN - 1) / kBN);
@@ -879,7 +916,7 @@ int launch_pair(const uint8_t* a, const uint8_t* w, Params p, int dev, cudaStrea
   cudaLaunchAttribute attr[2] = {pdl_attr(), cluster_attr(2)};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel, mA, mB, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel, mA, mB, mY, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
 }
@@ -922,9 +959,10 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 //   cluster's joint sum 600 + 200 S + 8 NT.
 // Few tokens to a tile fill the GPU and share little; the pair kernel shares
 // most and pays from about 75 tiles of 256 x 256.  For instance 512 x 4096 x
-// 4096: 16.8 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and S = 2;
-// 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096: 56.1 us by
-// pairs, 66.0 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32, 13.6 by pairs.
+// 4096: 16.8 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and S
+// = 2; 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096:
+// 56.1 us by pairs, 66.0 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32,
+// 13.6 by pairs.
 struct Plan {
   int NT, S;                // tokens to a tile (0: the pair kernel), CTAs to a cluster
 };
@@ -977,7 +1015,7 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
                : p.kbs % 4 == 0 && aligned(a_scales, 4) && aligned(w_scales, 4)  ? 4
                                                                                   : 1;
   p.y_four = N % 4 == 0 && aligned(Y, 8);
-  p.y_vec = N % 16 == 0 && aligned(Y, 32) ? 2 : N % 8 == 0 && aligned(Y, 16) ? 1 : 0;
+  p.y_tma = N % 8 == 0 && aligned(Y, 16);
   int rc = device_error_word_ptr(&p.err);
   if (rc != RBQ_OK) return rc;
   int dev = 0, sms = 148;

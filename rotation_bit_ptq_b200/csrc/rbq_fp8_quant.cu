@@ -24,11 +24,11 @@ using sm100::griddep_launch_dependents;
 using sm100::griddep_wait;
 
 // The row kernels: a thread holds 32 consecutive values of a row (of which the
-// second 16 may lie behind its end: d is a multiple of 16), and the 4 threads of a
-// block of 128 find its maximum by shuffles.  What a thread does besides its
-// values (its place, shuffles, scales) is paid half as often as with 16
-// values: 32760 x 8960 with GELU and checkpoint took 243 us with 16 values, 223 with
-// 32 in CTAs of 256 threads and 207 in CTAs of 128, eight to an SM.
+// second 16 may lie behind its end: d is a multiple of 16), and the 4 threads
+// of a block of 128 find its maximum by shuffles.  What a thread does besides
+// its values (its place, shuffles, scales) is paid half as often as with 16
+// values: 32760 x 8960 with GELU and checkpoint took 243 us with 16 values, 223
+// with 32 in CTAs of 256 threads and 207 in CTAs of 128, eight to an SM.
 constexpr int kVals = 32;
 constexpr int kRowThreads = 128, kRowCtas = 8;
 constexpr int kLanesPerBlock = kBlock / kVals;

@@ -23,6 +23,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <cmath>
 #include <utility>
 
 #include "rbq_fp8.cuh"
@@ -112,8 +114,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   WTail* tl = reinterpret_cast<WTail*>(ops + kWStages * kWStage);
   const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int work0 = static_cast<int>(cluster_id_x()), wstep = static_cast<int>(cluster_count_x());
+  // clusters are pairs of neighbouring blocks; the compiler knows that these are the same in all threads
+  const uint32_t rank = blockIdx.x & 1u;
+  const int work0 = static_cast<int>(blockIdx.x >> 1), wstep = static_cast<int>(gridDim.x >> 1);
   const int ntiles_n = (p.N + kTileN - 1) / kTileN, ntiles_k = (p.K + BK - 1) / BK;
   const int ntiles = ntiles_n * ntiles_k, nwork = ntiles * p.parts;
   const int slices = (p.M + kTok - 1) / kTok;
@@ -140,37 +143,40 @@ __global__ void __launch_bounds__(kWThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = tl->tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tl->tmem_slot, 0);
   griddep_wait();
   griddep_launch_dependents();
 
   if (warp == kWMmaWarp) {
-    if (rank == 0 && elect_one()) {
-      issuer = true;
+    if (rank == 0) {       // the warp goes through the loop together, one thread issues
       const uint64_t desc0 = sdesc_mn_sw128(smem_u32(ops));
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
       for (int w = work0; w < nwork && ok; w += wstep, ++it) {
         const uint32_t a = it & 1u, use = it >> 1;
-        if (use >= 1 && !mbar_wait_or_abort_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
+        if (use >= 1 && !mbar_warp_wait_cl(&tl->acc_empty[a], (use - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t acc = tmem + a * BK;
         int first, last;
         part_range(slices, p.parts, w / ntiles, first, last);
         for (int t = first; t < last; ++t) {
-          if (!mbar_wait_or_abort(&tl->full[s], ph, abort)) { ok = false; break; }
+          if (!mbar_warp_wait(&tl->full[s], ph, abort)) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = desc0 + ((s * static_cast<uint32_t>(kWStage)) >> 4);
           const uint64_t bd = ad + (G::kA >> 4);
+          const uint32_t add = t != first;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)          // 16 tokens = two atoms of 8
-            umma_f16_pair(acc, ad + k * (2048 >> 4), bd + k * (2048 >> 4), G::kIdesc, k != 0 || t != first);
-          umma_commit_pair(&tl->empty[s], 3);
+            for (int k = 0; k < kTok / 16; ++k)          // 16 tokens = two atoms of 8
+              umma_f16_pair(acc, ad + k * (2048 >> 4), bd + k * (2048 >> 4), G::kIdesc, k != 0 ? 1u : add);
+            umma_commit_pair(&tl->empty[s], 3);
+          }
           if (++s == kWStages) { s = 0; ph ^= 1u; }
         }
-        if (ok) umma_commit_pair(&tl->acc_full[a], 3);
+        if (ok && elect_one()) umma_commit_pair(&tl->acc_full[a], 3);
       }
-      if (!ok) atomicOr(p.err, 2u);
+      if (!ok && lane == 0) atomicOr(p.err, 2u);
+      issuer = elect_one();
     }
   } else if (warp == kWTmaWarp) {
     if (elect_one()) {
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tl->acc_empty[a], 0));
+      if (lane == 0) mbar_arrive_relaxed(mapa_shared(&tl->acc_empty[a], 0));
     }
   }
 
@@ -386,32 +392,33 @@ int launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool pair,
   return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
 }
 
-// The width of a tile and the parts the tokens are split into: what takes
-// least by a linear model, in ns, of the times of 15 gradients of 16 to 32760
-// tokens and 64 x 128 to 16384 x 4096 weights (its choice was the best or
-// within 7 % of it): `start` a launch, `slice` each 64 tokens, `wave` each
-// further wave of tiles, and for the joint sum 2300, 110 a part and 0.3 per
-// thousand fp32 values moved.  Narrow tiles are twice as many, wide ones read dY half as
-// often: 1560 x 1536 x 1536 takes 11.7 us with 128 (no parts), 15.9 with 256 and
-// 17.3 with 256 in two parts; 4096 x 16384 x 4096 332 us with 256, 366 with
-// 128; 3001 x 64 x 128 9.6 us in 5 parts, 13.1 in one.
+// The width of a tile and the parts the tokens are split into: what takes least
+// by a linear model, in ns, of the times of 15 gradients of 16 to 32760 tokens
+// and 64 x 128 to 16384 x 4096 weights (its choice was the best or within 7 %
+// of it): `start` a launch, `slice` each 64 tokens or what 17 TB/s take from L2
+// for all of them, `wave` each further wave of tiles, and for the joint sum
+// 2300, 110 a part and 0.3 per thousand fp32 values moved.  Narrow tiles are
+// twice as many, wide ones read dY half as often: 1560 x 1536 x 1536 takes 11.7
+// us with 128 (no parts), 15.9 with 256 and 17.3 with 256 in two parts; 4096 x
+// 16384 x 4096 332 us with 256, 366 with 128; 3001 x 64 x 128 9.6 us in 5
+// parts, 13.1 in one.
 struct WPlan {
   int BK, parts;
 };
 WPlan make_wplan(int M, int N, int K, int pairs) {
-  const auto waves = [](long long tiles, int n) { return (tiles + n - 1) / n; };
+  const auto up = [](double a, double b) { return std::ceil(a / b); };
   constexpr struct {
     int BK, start, wave, slice;
   } kinds[] = {{256, 4700, 2600, 310}, {128, 3600, 1300, 165}};
   const int slices = (M + kTok - 1) / kTok;
   WPlan best{256, 1};
-  long long least = -1;
+  double least = -1;
   for (const auto& k : kinds) {
-    const long long ntiles = ((N + 255LL) / 256) * ((K + k.BK - 1LL) / k.BK);
-    for (int parts = 1; parts <= slices && (parts == 1 || ntiles * parts <= pairs); ++parts) {
-      const long long w = waves(ntiles * parts, pairs);
-      const long long t = k.start + k.wave * (w - 1) + w * waves(slices, parts) * k.slice +
-                          (parts > 1 ? 2300 + 110 * parts + (parts + 1LL) * N * K * 3 / 10000 : 0);
+    const double tiles = up(N, 256) * up(K, k.BK), l2 = tiles * slices * ((256 + k.BK) * 2 * kTok) / 17000;
+    for (int parts = 1; parts <= slices && (parts == 1 || tiles * parts <= pairs); ++parts) {
+      const double waves = up(tiles * parts, pairs);
+      const double t = k.start + k.wave * (waves - 1) + std::max(waves * up(slices, parts) * k.slice, l2) +
+                       (parts > 1 ? 2300 + 110 * parts + (parts + 1.) * N * K * 3 / 10000 : 0);
       if (least < 0 || t < least) {
         least = t;
         best = {k.BK, parts};
