@@ -63,6 +63,12 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Two fp32 (their bits) -> one word of two BF16.
+__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // True in one thread of a converged warp, the one that issues its MMAs or its
 // TMA copies.  The operands of both are uniform registers: under a test of the
 // lane number the compiler moves each of them there by a loop over the threads
@@ -93,8 +99,19 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, con
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// This thread's bulk groups have read their shared memory / have been written.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(static_cast<uint32_t>(__cvta_generic_to_shared(src)))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last N of this thread's bulk groups have read their shared
+// memory; all of them have been written.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // As mbar_warp_wait, for a barrier that threads of the other CTA arrive on.
 __device__ __forceinline__ bool mbar_warp_wait_cl(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {

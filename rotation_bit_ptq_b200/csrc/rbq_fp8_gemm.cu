@@ -245,11 +245,6 @@ constexpr int kPiece = 32 * 128;          // bytes of a warp's 32 rows x 64 colu
 constexpr size_t kSmem = 1024 + kStages * kStage + kSfSlots * kSfSlot + 4 * kPiece + sizeof(Tail) + 64;
 static_assert(kSfSlots * kSfSlot % 1024 == 0, "pieces are swizzle atoms");
 
-__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A warp's 32 rows x 64 columns of the output (row m0 + lane in each lane, 32
 // words of two BF16) to rows whose length or address TMA does not take (N no
 // multiple of 8).  Row by lane, each 2-byte store of the warp falls into 32
@@ -515,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nb = nt * kBN + 64 * cc;
         if (m0 >= p.M || nb >= p.N) continue;           // the same in the whole warp
         if (p.y_tma) {
-          if (lane == 0) bulk_wait_read();              // the last piece has left
+          if (lane == 0) bulk_wait_read<0>();              // the last piece has left
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -951,18 +946,18 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 }
 
 // Which kernel, with how many tokens to a tile and how many CTAs to a tile's
-// K: what takes least by a linear model, in ns, of the times of 35 layers of 1
+// K: what takes least by a linear model, in ns, of the times of 42 layers of 1
 // to 32760 tokens, 64 to 16384 outputs and 256 to 16384 inputs with every
-// choice of both (its choice was the best or within 6 % of it in all of them):
-//   a launch `start`, each K slice of a wave of CTAs `slice` or what 17 TB/s take
-//   from L2 for all of them, each further wave 5000 (2400 by pairs), a
-//   cluster's joint sum 600 + 200 S + 8 NT.
+// choice of both (its choice was the best or within 3 % of it in all but one
+// of them, where it lost 12 %): a launch `start`, each K slice of a wave of
+// CTAs `slice` or what 17 TB/s take from L2 for all of them, each further wave
+// 5000 (2400 by pairs), a cluster's joint sum 600 + 200 S + 8 NT.
 // Few tokens to a tile fill the GPU and share little; the pair kernel shares
-// most and pays from about 75 tiles of 256 x 256.  For instance 512 x 4096 x
-// 4096: 16.8 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and S
-// = 2; 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096:
-// 56.1 us by pairs, 66.0 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32,
-// 13.6 by pairs.
+// most and pays from about 60 tiles of 256 x 256.  For instance 512 x 4096 x
+// 4096: 15.2 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and
+// S = 2; 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096:
+// 52.4 us by pairs, 65.9 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32,
+// 11.1 by pairs.
 struct Plan {
   int NT, S;                // tokens to a tile (0: the pair kernel), CTAs to a cluster
 };

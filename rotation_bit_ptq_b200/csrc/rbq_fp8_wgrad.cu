@@ -71,10 +71,8 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
 
 struct WParams {
   int M, N, K;
-  void* out;                  // [N, K] BF16 or fp32, or [parts, N, K] fp32
-  int f32;
+  int f32;                    // of the output, [parts, N, K]
   int parts;                  // token ranges, each summed apart
-  int out_vec;                // rows of `out` 32-byte aligned
   int order;
   unsigned int* err;
 };
@@ -89,8 +87,10 @@ struct __align__(8) WTail {
   volatile uint32_t abort;
 };
 
+constexpr int kPiece = 32 * 128;          // bytes of a warp's piece of the output: 32 rows x 64 BF16 or 32 fp32
 template <int BK>
-constexpr size_t kWSmem = 1024 + Wg<BK>::kStages * Wg<BK>::kStage + sizeof(WTail) + 64;
+constexpr size_t kWSmem = 1024 + Wg<BK>::kStages * Wg<BK>::kStage + 8 * kPiece + sizeof(WTail) + 64;
+static_assert(kWSmem<256> <= 227 * 1024 && kWSmem<128> <= 227 * 1024, "fits an SM");
 
 __device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
@@ -106,13 +106,15 @@ __device__ __forceinline__ void part_range(int slices, int parts, int part, int&
 
 template <int BK>
 __global__ void __launch_bounds__(kWThreads, 1)
-    wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX, const WParams p) {
+    wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
+                 const __grid_constant__ CUtensorMap tmW, const WParams p) {
   using G = Wg<BK>;
   constexpr int kWStages = G::kStages, kWStage = G::kStage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ops = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  WTail* tl = reinterpret_cast<WTail*>(ops + kWStages * kWStage);
+  uint8_t* pieces = ops + kWStages * kWStage;
+  WTail* tl = reinterpret_cast<WTail*>(pieces + 8 * kPiece);
   const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31;
   // clusters are pairs of neighbouring blocks; the compiler knows that these are the same in all threads
   const uint32_t rank = blockIdx.x & 1u;
@@ -206,8 +208,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (!ok) atomicOr(p.err, 16u);
     }
   } else {
-    const int r = 32 * warp + lane;
-    uint32_t it = 0;
+    // The output leaves by TMA, which writes whole lines and cuts what lies
+    // outside: a warp's 32 rows in pieces of 128 bytes, two of them in turn.
+    // (Row by lane in 32-byte stores, the 4096 x 16384 gradient of 64 tokens
+    // took 48 us in place of 29.)
+    uint32_t it = 0, pieces_out = 0;
+    const auto put = [&](const uint32_t (&o)[32], int x, int y, int z) {
+      uint8_t* piece = pieces + (2 * warp + (pieces_out++ & 1u)) * kPiece;
+      if (lane == 0) bulk_wait_read<1>();               // the piece before the last has left
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(piece + sw128_offset(lane, j)) =
+            make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_3d(&tmW, x, y, z, piece);
+    };
     for (int w = work0; w < nwork; w += wstep, ++it) {
       const uint32_t a = it & 1u, use = it >> 1;
       if (!mbar_warp_wait(&tl->acc_full[a], use & 1, abort)) {
@@ -217,49 +234,34 @@ __global__ void __launch_bounds__(kWThreads, 1)
       tc_fence_after();
       int nt, kt;
       tiles::tile_coords(w % ntiles, ntiles_n, ntiles_k, p.order, nt, kt);
-      const int n = nt * kTileN + static_cast<int>(rank) * kHalf + r;
-      const long long row = static_cast<long long>(w / ntiles) * p.N + n;
+      const int n0 = nt * kTileN + static_cast<int>(rank) * kHalf + 32 * warp, part = w / ntiles;
 #pragma unroll 1
-      for (int cc = 0; cc < BK / 32; ++cc) {
-        uint32_t v[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * BK + 32 * cc, v);
+      for (int c = 0; c < BK / 64; ++c) {
+        uint32_t u[32], v[32];
+        const uint32_t t = tmem + (static_cast<uint32_t>(32 * warp) << 16) + a * BK + 64 * c;
+        tmem_ld32(t, u);
+        tmem_ld32(t + 32, v);
         tmem_wait_ld();
-        const int kc = kt * BK + 32 * cc;
-        if (n >= p.N || kc >= p.K) continue;
-        const int left = p.K - kc;                      // a multiple of 16
+        const int kc = kt * BK + 64 * c;
+        if (n0 >= p.N || kc >= p.K) continue;           // the same in the whole warp
         if (p.f32) {
-          float* dst = static_cast<float*>(p.out) + row * p.K + kc;
-          if (p.out_vec) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (8 * j < left) st_v8(dst + 8 * j, v + 8 * j);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < left) dst[j] = __uint_as_float(v[j]);
-          }
+          put(u, kc, n0, part);
+          if (kc + 32 < p.K) put(v, kc + 32, n0, part);
         } else {
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.K + kc;
-          uint32_t o[16];
+          uint32_t o[32];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+            o[j] = bf16x2(u[2 * j], u[2 * j + 1]);
+            o[16 + j] = bf16x2(v[2 * j], v[2 * j + 1]);
           }
-          if (p.out_vec) {
-            st_v8(dst, o);
-            if (left > 16) st_v8(dst + 16, o + 8);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < left) dst[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
-          }
+          put(o, kc, n0, part);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_relaxed(mapa_shared(&tl->acc_empty[a], 0));
     }
+    if (lane == 0) bulk_wait();
   }
 
   tc_fence_before();
@@ -300,28 +302,44 @@ __global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, 
   }
 }
 
-// out[i] = part 0 + part 1 + ... in that order.
+// out[i] = the sum of the parts: G groups of threads take every G-th part each,
+// in their order, and the groups' sums are added in theirs.  One group where
+// the parts are few; eight where they are many and the gradient small, so that
+// their loads do not wait for one another (256 x 256 in 27 parts: 9.7 us with
+// one group).
+template <int G>
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int nparts, long long n4, void* out,
                                                         int f32) {
+  constexpr int kOut = 256 / G;
+  __shared__ float4 sums[G > 1 ? 256 : 1];
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = blockIdx.x * 256ll + threadIdx.x;
-  if (i >= n4) return;
-  float4 s = parts[i];
-#pragma unroll 8
-  for (int q = 1; q < nparts; ++q) {
-    const float4 v = parts[q * n4 + i];
+  const int g = threadIdx.x / kOut, l = threadIdx.x % kOut;
+  const long long i = blockIdx.x * static_cast<long long>(kOut) + l;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](const float4& v) {
     s.x += v.x;
     s.y += v.y;
     s.z += v.z;
     s.w += v.w;
+  };
+  if (i < n4) {
+#pragma unroll 8
+    for (int q = g; q < nparts; q += G) add(parts[q * n4 + i]);
   }
+  if constexpr (G > 1) {
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int q = 1; q < G; ++q) add(sums[q * kOut + l]);
+  }
+  if (i >= n4) return;
   if (f32) {
     static_cast<float4*>(out)[i] = s;
   } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
-    static_cast<uint2*>(out)[i] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    static_cast<uint2*>(out)[i] = make_uint2(bf16x2(__float_as_uint(s.x), __float_as_uint(s.y)),
+                                             bf16x2(__float_as_uint(s.z), __float_as_uint(s.w)));
   }
 }
 
@@ -336,6 +354,21 @@ int encode_tokens_map(CUtensorMap* map, const uint16_t* base, int rows, int cols
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
+}
+
+// [parts, N, K] of BF16 or fp32, boxes of 32 rows x 128 bytes, 128B swizzle.
+int encode_out_map(CUtensorMap* map, void* base, int parts, int N, int K, bool f32) {
+  auto fn = qfast::encode_fn();
+  if (!fn) return RBQ_ECUDA;
+  const cuuint64_t row = (f32 ? 4 : 2) * static_cast<cuuint64_t>(K);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(parts)};
+  const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(N)};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
 }
 
@@ -465,25 +498,24 @@ int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M
   p.K = K;
   p.parts = parts;
   p.f32 = parts > 1 || f32;
-  p.out = parts > 1 ? part : dW;
-  p.out_vec = parts > 1 || aligned(dW, 32);      // rows are multiples of 16 values
   p.order = tiles::tile_order(dev, 2LL * M * N, 2LL * M * K);
   p.err = err;
-  CUtensorMap mY, mX;
+  CUtensorMap mY, mX, mW;
   if (rc == RBQ_OK) rc = encode_tokens_map(&mY, dY, M, N);
   if (rc == RBQ_OK) rc = encode_tokens_map(&mX, x, M, K);
+  if (rc == RBQ_OK) rc = encode_out_map(&mW, parts > 1 ? static_cast<void*>(part) : dW, parts, N, K, p.f32 != 0);
   if (rc == RBQ_OK) {
     const long long nwork = ntiles * parts;
     const dim3 grid(2 * static_cast<unsigned>(nwork < pairs ? nwork : pairs), 1, 1);
-    rc = plan.BK == 256 ? launch(wgrad_kernel<256>, grid, kWThreads, kWSmem<256>, true, st, mY, mX, p)
-                        : launch(wgrad_kernel<128>, grid, kWThreads, kWSmem<128>, true, st, mY, mX, p);
+    rc = plan.BK == 256 ? launch(wgrad_kernel<256>, grid, kWThreads, kWSmem<256>, true, st, mY, mX, mW, p)
+                        : launch(wgrad_kernel<128>, grid, kWThreads, kWSmem<128>, true, st, mY, mX, mW, p);
   }
   if (rc == RBQ_OK && parts > 1) {
-    const long long n4 = static_cast<long long>(N) * K / 4, grid = (n4 + 255) / 256;
+    const long long n4 = static_cast<long long>(N) * K / 4, per = parts > 4 ? 32 : 256, grid = (n4 + per - 1) / per;
     rc = grid > 0x7FFFFFFFll
              ? RBQ_EINVAL
-             : launch(sum_parts_kernel, dim3(static_cast<unsigned>(grid), 1, 1), 256, 0, false, st,
-                      reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
+             : launch(parts > 4 ? sum_parts_kernel<8> : sum_parts_kernel<1>, dim3(static_cast<unsigned>(grid), 1, 1), 256,
+                      0, false, st, reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
   }
   e = cudaFreeAsync(ws, st);
   if (rc == RBQ_OK && e != cudaSuccess) rc = cuda_fail(e);
