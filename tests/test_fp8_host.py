@@ -156,3 +156,21 @@ def test_binding_refuses_cpu_tensors():
 
 def test_fp8_blocks():
     assert [rbq.fp8_blocks(n) for n in (0, 1, 128, 129, 4096)] == [0, 1, 1, 2, 32]
+
+
+def test_native_binding_leaves_other_calls_alone():
+    """_rbq_call.so answers None -- make the call in Python -- for whatever is not
+    an ordinary call, and raises nothing."""
+    from rotation_bit_ptq_b200 import _fp8
+    native = _fp8._ordinary()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 64).to(torch.float8_e4m3fn), torch.ones(4, 1).to(torch.float8_e8m0fnu)
+    for f, calls in ((native.quantize_fp8, ((x, 0, False), (None, 0, False), (x,), (x, "gelu", False))),
+                     (native.quantize_weights_fp8, ((x, False), ([1.0], True), ())),
+                     (native.qlinear_fp8, ((q, s, q, s), (1, 2, 3, 4), (q, s))),
+                     (native.qlinear_fp8_wgrad, ((x, q, s, False), (None, q, s, False))),
+                     (native.gelu_backward_fp8, ((x, q, s, True), (x, q, None, True)))):
+        for args in calls:
+            assert f(*args) is None, args
+    with pytest.raises(TypeError):
+        native.bind(1, 2)

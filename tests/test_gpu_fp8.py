@@ -200,6 +200,59 @@ def test_gelu_backward_in_place():
     assert torch.equal(out, ref)
 
 
+def test_gelu_of_extreme_values():
+    """Zeros of both signs, subnormals, values far out on both sides, infinities
+    and NaN, each alone in its block."""
+    v = np.array([0.0, -0.0, 1e-40, -1e-40, 2.0 ** -126, 6.0, -6.0, 13.0, -13.0, 100.0, -100.0, 1e5, -1e5, 1e30, -1e30,
+                  3.3e38, -3.3e38, np.inf, -np.inf, np.nan], dtype=np.float32)
+    x = np.zeros((len(v), 128), dtype=np.float32)
+    x[:, 5] = v
+    q, s, xq, xs = rbq.quantize_fp8(torch.from_numpy(x).cuda(), activation="gelu", checkpoint=True)
+    with np.errstate(invalid="ignore"):
+        h = oracle.gelu(v.astype(np.float64))
+    got = _held(q, s)
+    fin = np.isfinite(h)
+    assert np.array_equal(np.isnan(got[:, 5]), ~fin)
+    # as test_quantize_gelu_and_checkpoint; below the smallest scale a code's step is 2^-9 2^-117
+    tol = np.maximum(2.0 ** -4 * np.abs(h), 2.0 ** -127) + 4e-7 * np.abs(v)
+    assert np.all(np.abs(got[:, 5] - h)[fin] <= tol[fin])
+    assert not np.nan_to_num(np.delete(got, 5, 1)).any()
+    with np.errstate(invalid="ignore"):
+        rq, re = oracle.fp8_encode(x)
+    assert np.array_equal(_exponents(xs), re) and np.array_equal(_code_values(xq), rq, equal_nan=True)
+
+
+def test_gelu_far_below_zero_keeps_its_digits():
+    """Blocks that hold nothing but x in [-7, -3], where GELU(x) is x times the
+    normal tail: the tail is known to 9e-4 of itself to -5 and 4e-3 to -7 (the fit's error,
+    computed in 64 bits over [0, 7] when it was made), and exp2 and the roundings of its argument, of
+    magnitude up to 43 and so 2^-19 each, add 9 * 2^-19 ln 2 + 2^-22 < 2e-5."""
+    x = np.linspace(-7, -3, 64 * 128, dtype=np.float32).reshape(64, 128)
+    q, s = rbq.quantize_fp8(torch.from_numpy(x).cuda(), activation="gelu")
+    h = oracle.gelu(x.astype(np.float64))
+    got, sc = _held(q, s), oracle.fp8_scales(_exponents(s), 1, x.shape)
+    rel = np.where(x >= -5, 9e-4, 4.2e-3) + 2e-5
+    assert np.all(np.abs(got - h) <= np.maximum(2.0 ** -4 * np.abs(h), 2.0 ** -10 * sc) + rel * np.abs(h) * (1 + 2.0 ** -4))
+
+
+def test_gelu_backward_of_what_is_not_finite():
+    """NaN in the checkpoint or the gradient reaches its own value and its own code only."""
+    g = np.random.default_rng(2)
+    xq, xs, _ = _random_codes(g, 6, 256)
+    dh = torch.randn(6, 256, device="cuda").bfloat16()
+    ref = rbq.gelu_backward_fp8(dh, xq, xs)
+    xq.view(torch.uint8)[1, 7], xq.view(torch.uint8)[2, 130] = 0x7F, 0xFF
+    dh[3, 9], dh[4, 200] = float("nan"), float("inf")
+    xs.view(torch.uint8)[5, 1] = 255
+    dx, q, s = rbq.gelu_backward_fp8(dh, xq, xs, quantize=True)
+    bad = torch.zeros(6, 256, dtype=torch.bool, device="cuda")
+    bad[1, 7] = bad[2, 130] = bad[3, 9] = bad[4, 200] = True
+    bad[5, 128:] = True
+    assert torch.equal(~torch.isfinite(dx), bad) and torch.equal(dx[~bad], ref[~bad])
+    rq, re = oracle.fp8_encode(dx.double().cpu().numpy())
+    assert np.array_equal(_exponents(s), re) and np.array_equal(_code_values(q), rq, equal_nan=True)
+
+
 # ---- the layer ------------------------------------------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (1, 1, 16), (1, 4096, 4096), (2, 1000, 2048), (15, 300, 1040),
@@ -215,6 +268,49 @@ def test_layer(M, N, K):
     y = rbq.qlinear_fp8(aq, asc, wq, wsc, out=out)
     assert y is out
     _close(bf16_to_numpy(y), a @ w.T, np.abs(a) @ np.abs(w).T, K / 32)
+
+
+# Enough tiles for the kernel of CTA pairs; rows of Y by TMA (N a multiple of
+# 8), of whole words (even N) and of halves; rows of scales that are
+# multiples of 16, of 4 and of nothing, in one slot of 16 slices and in several.
+@pytest.mark.parametrize("M,N,K", [(4097, 3001, 272), (4100, 3002, 528), (4096, 3004, 512), (4000, 3008, 2048),
+                                   (3000, 4104, 4112), (33000, 264, 144), (2305, 6001, 16)])
+def test_layer_of_many_tokens(M, N, K):
+    g = np.random.default_rng(M + N + K)
+    aq, asc, a = _random_codes(g, M, K)
+    wq, wsc, w = _random_codes(g, N, K, 128)
+    ref, absum = a @ w.T, np.abs(a) @ np.abs(w).T
+    for off in (0, 1, 2):                                   # elements from a 16-byte boundary
+        buf = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = rbq.qlinear_fp8(aq, asc, wq, wsc, out=buf[off:off + M * N].view(M, N))
+        _close(bf16_to_numpy(y), ref, absum, K / 32)
+        assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
+
+
+# Few tokens and a long K: split over a cluster, several slots of scales in each part.
+@pytest.mark.parametrize("M,N,K", [(5, 130, 16384), (1, 1000, 40000), (40, 64, 33024), (130, 72, 20480)])
+def test_layer_of_few_tokens_and_many_slices(M, N, K):
+    g = np.random.default_rng(M + N + K)
+    aq, asc, a = _random_codes(g, M, K)
+    wq, wsc, w = _random_codes(g, N, K, 128)
+    _close(bf16_to_numpy(rbq.qlinear_fp8(aq, asc, wq, wsc)), a @ w.T, np.abs(a) @ np.abs(w).T, K / 32)
+
+
+def test_scales_at_any_address():
+    """Scales that begin 1, 2, 3, 4 and 8 bytes from a boundary, at both ends of
+    their buffers, for both kernels."""
+    g = np.random.default_rng(8)
+    for M, N, K in ((9, 260, 2048), (4097, 2600, 2048), (4097, 2600, 640)):
+        aq, asc, a = _random_codes(g, M, K)
+        wq, wsc, w = _random_codes(g, N, K, 128)
+        ref = rbq.qlinear_fp8(aq, asc, wq, wsc)
+        for off in (1, 2, 3, 4, 8):
+            moved = []
+            for t in (asc, wsc):
+                buf = torch.zeros(t.numel() + off, dtype=torch.uint8, device="cuda")
+                buf[off:] = t.view(torch.uint8).flatten()
+                moved.append(buf[off:].view(E8).view(t.shape))
+            assert torch.equal(rbq.qlinear_fp8(aq, moved[0], wq, moved[1]), ref)
 
 
 def test_layer_uses_each_scale():
@@ -268,6 +364,13 @@ def test_weight_gradient(M, N, K, dtype):
     got = dW.double().cpu().numpy()
     tol = (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23) * np.abs(ref) + (M / 16 + 8) * 2.0 ** -21 * absum
     assert np.all(np.abs(got - ref) <= tol), float(np.max(np.abs(got - ref) / tol))
+
+
+# Wide tiles, narrow ones in several parts, and the last token alone in its slice.
+@pytest.mark.parametrize("M,N,K", [(300, 4096, 4096), (4097, 512, 1040), (6000, 40, 48), (20001, 264, 272)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weight_gradient_tiles_and_parts(M, N, K, dtype):
+    test_weight_gradient(M, N, K, dtype)
 
 
 def test_weight_gradient_is_the_difference_of_the_loss():
@@ -395,6 +498,35 @@ def test_more_than_2_31_elements():
         _close(bf16_to_numpy(rows), av @ wv.T, np.abs(av) @ np.abs(wv).T, 1)
 
 
+def test_native_and_checked_calls_agree():
+    """The ordinary call (made by _rbq_call.so) and the one with buffers given
+    (made in Python) are the same call."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(300, 400, device="cuda", generator=g).bfloat16()
+    w = torch.nn.Parameter(torch.randn(272, 400, device="cuda", generator=g))
+    dy = torch.randn(300, 272, device="cuda", generator=g).bfloat16()
+
+    def like(*ts):
+        return [torch.full_like(t.view(torch.uint8), 0x55).view(t.dtype) for t in ts]
+
+    a = rbq.quantize_fp8(x, activation="gelu")
+    ca, cs = like(*a)
+    assert _same(a, rbq.quantize_fp8(x, activation="gelu", codes=ca, scale=cs)) and _same(a, (ca, cs))
+    wq = rbq.quantize_weights_fp8(w)
+    assert all(not t.requires_grad for t in wq)
+    cw, cws = like(*wq)
+    assert _same(wq, rbq.quantize_weights_fp8(w, codes=cw, scale=cws))
+    y = rbq.qlinear_fp8(*a, *wq)
+    assert torch.equal(y, rbq.qlinear_fp8(*a, *wq, out=torch.empty_like(y)))
+    for dtype in (torch.bfloat16, torch.float32):
+        dW = rbq.qlinear_fp8_wgrad(dy, *a, dtype=dtype)
+        assert dW.dtype == dtype and torch.equal(dW, rbq.qlinear_fp8_wgrad(dy, *a, out=torch.empty_like(dW)))
+    ck = rbq.quantize_fp8(x, activation="gelu", checkpoint=True)
+    dx = rbq.gelu_backward_fp8(x, *ck[2:])
+    assert torch.equal(dx, rbq.gelu_backward_fp8(x, *ck[2:], out=torch.empty_like(dx)))
+    assert _same(ck[:2], a)
+
+
 # ---- streams, graphs, repeated calls ---------------------------------------------------------
 
 def _step(x, w, dy):
@@ -417,7 +549,7 @@ def _step_inputs(M, K, N, seed):
             torch.randn(M, N, device="cuda", generator=g).bfloat16())
 
 
-@pytest.mark.parametrize("M,K,N", [(5, 256, 384), (700, 1040, 272)])
+@pytest.mark.parametrize("M,K,N", [(5, 256, 384), (700, 1040, 272), (4200, 1040, 2048)])
 def test_results_do_not_depend_on_the_run_or_the_stream(M, K, N):
     ins = [_step_inputs(M, K, N, i) for i in range(2)]
     ref = [_step(*i) for i in ins]
@@ -448,7 +580,7 @@ def test_stream_argument():
     assert _same((*a, *wq, y, dh, *dx, dW), ref)
 
 
-@pytest.mark.parametrize("M,K,N", [(3, 512, 1024), (700, 1040, 272)])
+@pytest.mark.parametrize("M,K,N", [(3, 512, 1024), (700, 1040, 272), (4200, 1040, 2048)])
 def test_captured_steps_share_nothing(M, K, N):
     """Two graphs of the whole step, replayed in turn and together on new inputs."""
     ins = [_step_inputs(M, K, N, i) for i in range(2)]
