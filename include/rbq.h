@@ -469,6 +469,9 @@ int quantize_rotated(const void* Xrot, int dtype, int T, int d, int bits, void* 
  * amax the largest finite |value| of the block, and round value / s to
  * nearest even.  NaN and infinities become NaN codes (0x7F / 0xFF) and do not
  * count for amax.  Every decoded value is exact in BF16.
+ *
+ * The first call of an entry point on a device sets its kernels up and may
+ * allocate the library's device error word: make it before a stream capture.
  */
 
 /*

@@ -85,9 +85,17 @@ def _matrix(t, name, dtype=None):
     return dev
 
 
+def check_stream_device(stream, dev):
+    """A stream of the operands' device (a launch goes to the stream's device,
+    which would read the operands through another's addresses)."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is of {stream.device}, the operands are of cuda:{dev}")
+
+
 def _call(name, dev, stream, *args):
     """lib().name(*args, stream) with device number `dev` current."""
     import torch
+    check_stream_device(stream, dev)
     fn = getattr(lib(), name)
     if stream is None and torch._C._cuda_getDevice() == dev:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
@@ -103,6 +111,7 @@ def _out(t, shape, dtype, like, stream, name, torch):
     if t is None:
         if stream is None:
             return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+        check_stream_device(stream, like.get_device())
         with _on(like.device, stream):
             return torch.empty(shape, dtype=dtype, device=like.device)
     if _operand(t, name, dtype) != like.get_device():

@@ -117,7 +117,8 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
 // whose rows have 70 scales, took 38 us by pairs in place of 31.)  Loaded words
 // may hold bytes of the rows beside it, but never of anything outside the
 // matrix of scales [lo, hi); what follows the row's last slice is not
-// multiplied.
+// multiplied.  Plain loads, not read-only ones: the kernel before may still be
+// writing the scales when this one is launched.
 template <int ALIGN>
 struct ScaleRow {
   static constexpr int kWords = ALIGN == 1 ? kGroups + 1 : kGroups;
@@ -137,23 +138,23 @@ struct ScaleRow {
     for (int q = 0; q < kWords; ++q) w[q] = 0u;
     if (!row) return;
     if constexpr (ALIGN == 16) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row));
+      const uint4 v = *reinterpret_cast<const uint4*>(row);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else if constexpr (ALIGN == 4) {
 #pragma unroll
       for (int q = 0; q < kGroups; ++q)
-        if (kGroup * q < left) w[q] = __ldg(reinterpret_cast<const uint32_t*>(row) + q);
+        if (kGroup * q < left) w[q] = reinterpret_cast<const uint32_t*>(row)[q];
     } else {
       const uint8_t* p = row - offset();
 #pragma unroll
       for (int q = 0; q < kWords; ++q, p += kGroup) {
         if (kGroup * q >= left + static_cast<int>(offset())) break;
         if (p >= lo && p + kGroup <= hi) {
-          w[q] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          w[q] = *reinterpret_cast<const uint32_t*>(p);
         } else {
 #pragma unroll
           for (int j = 0; j < kGroup; ++j)
-            if (p + j >= lo && p + j < hi) w[q] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+            if (p + j >= lo && p + j < hi) w[q] |= static_cast<uint32_t>(p[j]) << (8 * j);
         }
       }
     }

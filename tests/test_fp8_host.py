@@ -174,3 +174,17 @@ def test_native_binding_leaves_other_calls_alone():
             assert f(*args) is None, args
     with pytest.raises(TypeError):
         native.bind(1, 2)
+
+
+def test_streams_of_another_device_are_refused():
+    """Nothing is allocated or launched on a stream whose device is not the operands'."""
+    from types import SimpleNamespace
+
+    from rotation_bit_ptq_b200 import _fp8
+    stream = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    _fp8.check_stream_device(None, 0)
+    _fp8.check_stream_device(stream, 1)
+    with pytest.raises(ValueError):
+        _fp8.check_stream_device(stream, 0)
+    with pytest.raises(ValueError):
+        _fp8._call("quantize_fp8", 0, stream, None, rbq.RBQ_BF16, 0, 64, NONE, None, None, None, None)
