@@ -16,7 +16,7 @@
 // hand-over) into the 32 x 16 byte blocks tcgen05.cp replicates over the four
 // lane quadrants: the word of row r at 16 (r % 32) + 4 (r / 32).
 //
-// Two kernels, chosen by make_plan.
+// Three kernels, chosen by make_plan.
 // 1. fp8_pair_kernel (many tokens): persistent, on CTA pairs, 256 x 256 tiles
 //    (cta_group::2), K slices of 128, 6 stages of 32 KB per CTA.  Warps 0..3
 //    epilogue, 4 MMA issuer, 5 TMA producer, 6..9 scale loaders.  Two
@@ -31,6 +31,7 @@
 //    a cluster split K, each summing its part; the partial sums meet through
 //    distributed shared memory in a fixed order.  1 x 4096 x 4096 takes 4.9 us
 //    with the weights in L2 and 6.3 from HBM, 1 x 16384 x 4096 12.4 us (5.4 TB/s).
+// 3. fp8_dot_kernel (one to four tokens and not too many weights): CUDA cores.
 //
 // Every mbarrier wait is bounded; a thread whose wait runs out raises a shared
 // abort flag, records an error in the library's device error word, and the
@@ -840,6 +841,117 @@ int encode_out_map(CUtensorMap* map, uint16_t* base, int M, int N) {
   return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
 }
 
+// ---- single tokens ---------------------------------------------------------------
+// Up to four tokens on the CUDA cores: a CTA of 128 threads takes four weight
+// rows, a thread 16 codes of each (and the 16 that lie 2048 on), all rows'
+// loads in flight together.  Products of codes are exact in fp32 and are summed
+// by 16, two to an instruction; then come the two scales, and the sum over the
+// CTA in a fixed order.  No tensor maps, no tensor memory, no cluster: besides
+// the weights' way a token pays for a launch and one reduction.  1 x 4096 x
+// 4096 takes 4.2 us (5.3 from HBM) and fp8_few_kernel 4.9 (6.1); 1 x 1536 x
+// 1536 2.0 and 3.6; with more tokens or weights the tensor cores win (4 x
+// 4096 x 4096: 8.3 and 4.9).  Eight rows or several groups of threads to a
+// CTA, or 4096 codes at once, were slower: 4.6 to 6.9 us.
+constexpr int kDotThreads = 128, kDotRows = 4, kDotTokens = 4;
+constexpr int kDotSpan = 16 * kDotThreads;        // codes of a row that a CTA takes at a time
+
+using f2 = unsigned long long;                    // two fp32 in one 64-bit register
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Sixteen codes -> pairs of fp32.
+__device__ __forceinline__ void decode16(const uint4& c, f2 (&v)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 t = decode2(w[i / 2] >> (16 * (i & 1)));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(t.x), "f"(t.y));
+  }
+}
+// sum * 2^(xb - 127) * 2^(wb - 127) for any scale bytes: one factor after the
+// other, so that nothing overflows or loses digits on the way to a result that
+// does not.
+__device__ __noinline__ float scaled(float sum, uint32_t xb, uint32_t wb) {
+  const float lo = scale_value(min(xb, wb)), hi = scale_value(max(xb, wb));
+  return xb + wb > 254u ? sum * lo * hi : sum * hi * lo;
+}
+
+template <int MT>
+__global__ void __launch_bounds__(kDotThreads) fp8_dot_kernel(const uint8_t* a, const uint8_t* w, const Params p) {
+  __shared__ float sums[kDotThreads / 32][kDotRows * MT];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n0 = blockIdx.x * kDotRows, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // rows behind the last one repeat it and are not written
+  const uint8_t *rows[kDotRows], *scales[kDotRows];
+#pragma unroll
+  for (int r = 0; r < kDotRows; ++r) {
+    const int n = min(n0 + r, p.N - 1);
+    rows[r] = w + static_cast<long long>(n) * p.K;
+    scales[r] = p.sw + static_cast<long long>(n / kBlock) * p.kbs;
+  }
+  float acc[kDotRows][MT] = {};
+  for (long long k = 16 * threadIdx.x; k < p.K; k += kDotSpan) {
+    uint4 c[kDotRows], xc[MT];
+    uint32_t wb[kDotRows], xb[MT];
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r) {
+      c[r] = *reinterpret_cast<const uint4*>(rows[r] + k);
+      wb[r] = scales[r][k / kBlock];
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = min(m, p.M - 1);
+      xc[m] = *reinterpret_cast<const uint4*>(a + static_cast<long long>(row) * p.K + k);
+      xb[m] = p.sa[static_cast<long long>(row) * p.kbs + k / kBlock];
+    }
+    // whether each pair of scales has a product within 2^-100 and 2^100
+    uint32_t least_w = wb[0], most_w = wb[0], least_x = xb[0], most_x = xb[0];
+#pragma unroll
+    for (int r = 1; r < kDotRows; ++r) least_w = min(least_w, wb[r]), most_w = max(most_w, wb[r]);
+#pragma unroll
+    for (int m = 1; m < MT; ++m) least_x = min(least_x, xb[m]), most_x = max(most_x, xb[m]);
+    const bool near = least_w + least_x >= 154u && most_w + most_x <= 354u && max(most_w, most_x) < 255u;
+    f2 x[MT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) decode16(xc[m], x[m]);
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r) {
+      f2 v[8];
+      decode16(c[r], v);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f2 s = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fma2(v[i], x[m][i], s);
+        float even, odd;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(even), "=f"(odd) : "l"(s));
+        acc[r][m] = near ? fmaf(even + odd, __uint_as_float((xb[m] + wb[r] - 127u) << 23), acc[r][m])
+                         : acc[r][m] + scaled(even + odd, xb[m], wb[r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kDotRows; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[r][m] += __shfl_xor_sync(0xffffffffu, acc[r][m], o);
+      if (lane == 0) sums[warp][r * MT + m] = acc[r][m];
+    }
+  __syncthreads();
+  if (threadIdx.x < kDotRows * MT) {
+    const int r = threadIdx.x / MT, m = threadIdx.x % MT;
+    float s = sums[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kDotThreads / 32; ++i) s += sums[i][threadIdx.x];
+    if (m < p.M && n0 + r < p.N)
+      p.Y[static_cast<long long>(m) * p.N + n0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+  }
+}
+
 // uint8 [rows, K] K-major, boxes of box_rows x 128 bytes, 128B swizzle.
 int encode_map(CUtensorMap* map, const uint8_t* base, int rows, int K, int box_rows) {
   auto fn = qfast::encode_fn();
@@ -962,10 +1074,16 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 // S = 2; 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096:
 // 52.4 us by pairs, 65.9 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32,
 // 11.1 by pairs.
+// One to four tokens: fp8_dot_kernel where 1200 + 0.15 N + (250 + 260 M) for
+// each 2048 codes of a row + (45 + 80 M) for a million weights is less (30
+// layers of 64 to 16384 outputs and 256 to 16384 inputs: the better kernel
+// in all of them).
+constexpr int kDotPlan = -1;
 struct Plan {
-  int NT, S;                // tokens to a tile (0: the pair kernel), CTAs to a cluster
+  int NT, S;                // tokens to a tile (0: the pair kernel, kDotPlan), CTAs to a cluster
 };
-Plan make_plan(int M, int N, int kbs, int sms) {
+Plan make_plan(int M, int N, int K, int sms) {
+  const int kbs = blocks(K);
   const auto up = [](double a, double b) { return std::ceil(a / b); };
   const double pair_waves = up(up(M, 256) * up(N, 256), sms / 2);
   Plan best{0, 1};
@@ -987,7 +1105,23 @@ Plan make_plan(int M, int N, int kbs, int sms) {
     }
     if (k.NT >= M) break;
   }
+  if (M <= kDotTokens && 1200 + 0.15 * N + (250 + 260 * M) * up(K, kDotSpan) + (45 + 80 * M) * 1e-6 * N * K < least)
+    best = {kDotPlan, 1};
   return best;
+}
+
+template <int MT>
+int launch_dot(const uint8_t* a, const uint8_t* w, const Params& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + kDotRows - 1) / kDotRows), 1, 1);
+  cfg.blockDim = dim3(kDotThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_dot_kernel<MT>, a, w, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? RBQ_OK : cuda_fail(e);
 }
 
 }  // namespace
@@ -1023,11 +1157,15 @@ extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, cons
   if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const fp8::Plan plan = fp8::make_plan(M, N, p.kbs, sms);
+  const fp8::Plan plan = fp8::make_plan(M, N, K, sms);
   const int S = plan.S;
   for (int r = 1; r < S; ++r)
     while (static_cast<long long>(p.kbs) * r / S % p.sf_align) p.sf_align = p.sf_align == 16 ? 4 : 1;
   switch (plan.NT) {
+    case fp8::kDotPlan:
+      return M == 1   ? fp8::launch_dot<1>(a_codes, w_codes, p, st)
+             : M == 2 ? fp8::launch_dot<2>(a_codes, w_codes, p, st)
+                      : fp8::launch_dot<4>(a_codes, w_codes, p, st);
     case 16: return fp8::launch_few<16>(a_codes, w_codes, p, S, dev, st);
     case 32: return fp8::launch_few<32>(a_codes, w_codes, p, S, dev, st);
     case 64: return fp8::launch_few<64>(a_codes, w_codes, p, S, dev, st);

@@ -520,8 +520,8 @@ int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M
     const long long n4 = static_cast<long long>(N) * K / 4, per = parts > 4 ? 32 : 256, grid = (n4 + per - 1) / per;
     rc = grid > 0x7FFFFFFFll
              ? RBQ_EINVAL
-             : launch(parts > 4 ? sum_parts_kernel<8> : sum_parts_kernel<1>, dim3(static_cast<unsigned>(grid), 1, 1), 256,
-                      0, false, st, reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
+             : launch(parts > 4 ? sum_parts_kernel<8> : sum_parts_kernel<1>, dim3(static_cast<unsigned>(grid), 1, 1),
+                      256, 0, false, st, reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
   }
   e = cudaFreeAsync(ws, st);
   if (rc == RBQ_OK && e != cudaSuccess) rc = cuda_fail(e);

@@ -255,7 +255,8 @@ def test_gelu_backward_of_what_is_not_finite():
 
 # ---- the layer ------------------------------------------------------------------------
 
-@pytest.mark.parametrize("M,N,K", [(1, 128, 128), (1, 1, 16), (1, 4096, 4096), (2, 1000, 2048), (15, 300, 1040),
+@pytest.mark.parametrize("M,N,K", [(1, 128, 128), (1, 1, 16), (1, 1536, 1536), (1, 1001, 2064), (2, 999, 1552),
+                                   (3, 130, 4112), (4, 33, 6000), (4, 1002, 272), (2, 64, 8960), (1, 4096, 4096), (2, 1000, 2048), (15, 300, 1040),
                                    (16, 256, 512), (17, 129, 272), (33, 1001, 640), (64, 512, 1536), (65, 130, 400),
                                    (128, 384, 2064), (129, 127, 128), (255, 500, 1552), (256, 256, 8960),
                                    (257, 256, 128), (300, 1001, 1552), (511, 8, 4096), (513, 264, 656),
@@ -335,8 +336,30 @@ def test_layer_uses_each_scale():
         assert np.array_equal(bf16_to_numpy(y), ref)
 
 
+def test_layer_with_far_scales():
+    """Scales at the ends of what the quantisers choose, whose product is an
+    ordinary number (or, both small, the smallest): single products, exact."""
+    N, K = 260, 1552
+    kb = rbq.fp8_blocks(K)
+    g = np.random.default_rng(6)
+    for rows in (1, 2, 4, 9, 300, 4100):
+        q = np.zeros((rows, K), dtype=np.float32)
+        blk = np.arange(rows) % kb
+        q[np.arange(rows), blk * 128] = 1.0
+        e = g.choice([10, 20, 127, 200, 247], (rows, kb))
+        ew = g.choice([10, 20, 127, 200, 247], (rbq.fp8_blocks(N), kb))
+        y = rbq.qlinear_fp8(torch.from_numpy(q).cuda().to(F8), torch.from_numpy(e.astype(np.uint8)).cuda().view(E8),
+                            torch.ones(N, K, device="cuda").to(F8),
+                            torch.from_numpy(ew.astype(np.uint8)).cuda().view(E8))
+        exp = e[np.arange(rows), blk][:, None] - 127 + ew[np.arange(N) // 128][:, blk].T - 127
+        sure = (exp >= -126) & (exp <= 127)
+        got = bf16_to_numpy(y)
+        assert np.array_equal(got[sure], np.ldexp(1.0, exp)[sure]), rows
+        assert np.all(np.abs(got[exp < -126]) <= 2.0 ** -126) and np.all(np.isinf(got[exp > 127]))
+
+
 def test_layer_nan_scales_and_codes_reach_only_their_rows():
-    for M in (5, 300):
+    for M in (4, 5, 300):
         g = np.random.default_rng(M)
         aq, asc, a = _random_codes(g, M, 640)
         wq, wsc, w = _random_codes(g, 256, 640, 128)
