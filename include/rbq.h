@@ -477,7 +477,7 @@ int quantize_rotated(const void* Xrot, int dtype, int T, int d, int bits, void* 
 /*
  * quantize_fp8 -- codes and scales of the rows of act(X).
  *   X          device [T, d], RBQ_BF16 or RBQ_F32, 16-byte aligned
- *   T, d       rows (0 is a valid no-op); width, a multiple of 16
+ *   T, d       rows (0 is a valid no-op); width, a multiple of 16, at most 2^30
  *   activation RBQ_ACT_NONE or RBQ_ACT_GELU (fp32; |error| <= 1e-7 |x|, and
  *              for x in [-7, 0) <= 5e-3 of the value itself)
  *   codes      device uint8 [T, d], 16-byte aligned
@@ -492,7 +492,7 @@ int quantize_fp8(const void* X, int dtype, int T, int d, int activation, uint8_t
 /*
  * quantize_weights_fp8 -- codes and scales of a weight matrix.
  *   W        device [N, K], RBQ_BF16 or RBQ_F32, 16-byte aligned
- *   K        a multiple of 16
+ *   N, K     at most 2^30; K a multiple of 16
  *   codes    device uint8 [N, K], 16-byte aligned
  *   scales   device uint8 [ceil(N / 128), ceil(K / 128)]
  *   codes_t, scales_t  the same of W^T ([K, N] and [ceil(K / 128),
@@ -510,7 +510,7 @@ int quantize_weights_fp8(const void* W, int dtype, int N, int K, uint8_t* codes,
  * gradient of a layer is the same call on the codes of dY and of W^T.
  *   a_codes, a_scales  device, [M, K] and [M, ceil(K / 128)]
  *   w_codes, w_scales  device, [N, K] and [ceil(N / 128), ceil(K / 128)]
- *   M, N     at most 2^30; K a multiple of 16
+ *   M, N, K  at most 2^30; K a multiple of 16
  *   Y        device uint16 BF16 [M, N]
  * Alignment: codes 16-byte.  No workspace.
  * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
@@ -524,6 +524,7 @@ int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* 
  * on BF16 operands (the decoded codes are exact in BF16), fp32 accumulation.
  *   dY                 device uint16 BF16 [M, N], 16-byte aligned; N a multiple of 8
  *   a_codes, a_scales  device, [M, K] and [M, ceil(K / 128)]; K a multiple of 16
+ *   M, N, K            at most 2^30
  *   dW                 device [N, K], `dtype` RBQ_BF16 or RBQ_F32, 16-byte
  *                      aligned; overwritten (zeros when M is 0)
  * Workspace from a stream-ordered memory pool: M*K*2 bytes, and 4*N*K for each
@@ -536,7 +537,8 @@ int qlinear_fp8_wgrad(const uint16_t* dY, const uint8_t* a_codes, const uint8_t*
 /*
  * gelu_backward_fp8 -- the GELU's backward pass from the 8-bit checkpoint of
  * its input:  dX = bf16( dH (Phi(x) + x phi(x)) ),  x = code * s.
- *   dH                 device uint16 BF16 [T, d], 16-byte aligned; d a multiple of 16
+ *   dH                 device uint16 BF16 [T, d], 16-byte aligned; d a multiple of 16,
+ *                      at most 2^30
  *   x_codes, x_scales  device, from quantize_fp8 (x_codes 16-byte aligned)
  *   dX                 device uint16 BF16 [T, d], 16-byte aligned; may be dH itself
  *   codes, scales      the codes and scales of dX (as quantize_fp8 gives

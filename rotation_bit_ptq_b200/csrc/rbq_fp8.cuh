@@ -28,7 +28,7 @@ namespace rbq {
 namespace fp8 {
 
 constexpr int kBlock = 128;            // values per scale along a row (and rows per scale of a weight)
-constexpr int kMaxRows = 1 << 30;      // rows of an operand: tile coordinates stay in 32 bits
+constexpr int kMaxSize = 1 << 30;      // rows and columns of an operand: block counts and coordinates stay in 32 bits
 constexpr uint32_t kMinScale = 10;     // 2^-117
 constexpr uint32_t kMaxScale = 247;    // 2^120: amax up to the largest fp32
 

@@ -1132,7 +1132,8 @@ using namespace rbq;
 
 extern "C" int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                            const uint8_t* w_scales, int M, int N, int K, uint16_t* Y, void* stream) {
-  if (M < 0 || M > fp8::kMaxRows || N < 0 || N > fp8::kMaxRows || K <= 0 || K % 16) return RBQ_EINVAL;
+  if (M < 0 || M > fp8::kMaxSize || N < 0 || N > fp8::kMaxSize || K <= 0 || K > fp8::kMaxSize || K % 16)
+    return RBQ_EINVAL;
   if (M == 0 || N == 0) return RBQ_OK;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return RBQ_EINVAL;
   if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(Y, 2)) return RBQ_EALIGN;

@@ -512,7 +512,8 @@ using namespace rbq;
 
 extern "C" int quantize_fp8(const void* X, int dtype, int T, int d, int activation, uint8_t* codes, uint8_t* scales,
                             uint8_t* x_codes, uint8_t* x_scales, void* stream) {
-  if ((dtype != RBQ_BF16 && dtype != RBQ_F32) || T < 0 || d <= 0 || d % 16) return RBQ_EINVAL;
+  if ((dtype != RBQ_BF16 && dtype != RBQ_F32) || T < 0 || d <= 0 || d > fp8::kMaxSize || d % 16)
+    return RBQ_EINVAL;
   if (activation != RBQ_ACT_NONE && activation != RBQ_ACT_GELU) return RBQ_EINVAL;
   if (!x_codes != !x_scales || (x_codes && activation == RBQ_ACT_NONE)) return RBQ_EINVAL;
   if (T == 0) return RBQ_OK;
@@ -528,7 +529,8 @@ extern "C" int quantize_fp8(const void* X, int dtype, int T, int d, int activati
 
 extern "C" int quantize_weights_fp8(const void* W, int dtype, int N, int K, uint8_t* codes, uint8_t* scales,
                                     uint8_t* codes_t, uint8_t* scales_t, void* stream) {
-  if ((dtype != RBQ_BF16 && dtype != RBQ_F32) || N < 0 || K <= 0 || K % 16) return RBQ_EINVAL;
+  if ((dtype != RBQ_BF16 && dtype != RBQ_F32) || N < 0 || N > fp8::kMaxSize || K <= 0 || K > fp8::kMaxSize || K % 16)
+    return RBQ_EINVAL;
   if (!codes_t != !scales_t || (codes_t && N % 16)) return RBQ_EINVAL;
   if (N == 0) return RBQ_OK;
   if (!W || !codes || !scales) return RBQ_EINVAL;
@@ -540,7 +542,7 @@ extern "C" int quantize_weights_fp8(const void* W, int dtype, int N, int K, uint
 
 extern "C" int gelu_backward_fp8(const uint16_t* dH, const uint8_t* x_codes, const uint8_t* x_scales, int T, int d,
                                  uint16_t* dX, uint8_t* codes, uint8_t* scales, void* stream) {
-  if (T < 0 || d <= 0 || d % 16 || !codes != !scales) return RBQ_EINVAL;
+  if (T < 0 || d <= 0 || d > fp8::kMaxSize || d % 16 || !codes != !scales) return RBQ_EINVAL;
   if (T == 0) return RBQ_OK;
   if (!dH || !x_codes || !x_scales || !dX) return RBQ_EINVAL;
   if (!aligned(dH, 16) || !aligned(x_codes, 16) || !aligned(dX, 16) || (codes && !aligned(codes, 16)))

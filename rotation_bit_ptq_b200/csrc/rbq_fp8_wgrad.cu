@@ -536,7 +536,8 @@ using namespace rbq;
 
 extern "C" int qlinear_fp8_wgrad(const uint16_t* dY, const uint8_t* a_codes, const uint8_t* a_scales, int M, int N,
                                  int K, void* dW, int dtype, void* stream) {
-  if (M < 0 || M > fp8::kMaxRows || N < 0 || N > fp8::kMaxRows || N % 8 || K <= 0 || K % 16) return RBQ_EINVAL;
+  if (M < 0 || M > fp8::kMaxSize || N < 0 || N > fp8::kMaxSize || N % 8 || K <= 0 || K > fp8::kMaxSize || K % 16)
+    return RBQ_EINVAL;
   if (dtype != RBQ_BF16 && dtype != RBQ_F32) return RBQ_EINVAL;
   if (N == 0) return RBQ_OK;
   if (!dW) return RBQ_EINVAL;
