@@ -870,12 +870,12 @@ __device__ __forceinline__ void decode16(const uint4& c, f2 (&v)[8]) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(t.x), "f"(t.y));
   }
 }
-// sum * 2^(xb - 127) * 2^(wb - 127) for any scale bytes: one factor after the
-// other, so that nothing overflows or loses digits on the way to a result that
-// does not.
+// sum * 2^(xb - 127) * 2^(wb - 127) for any scale bytes, rounded once: taken one
+// after the other, the first factor can overflow, or cost digits, on the way to
+// a result that does neither (xb = 10, wb = 244 and a sum of 2^11).
 __device__ __noinline__ float scaled(float sum, uint32_t xb, uint32_t wb) {
-  const float lo = scale_value(min(xb, wb)), hi = scale_value(max(xb, wb));
-  return xb + wb > 254u ? sum * lo * hi : sum * hi * lo;
+  if (max(xb, wb) == 255u) return __uint_as_float(0x7FFFFFFFu);
+  return ldexpf(sum, static_cast<int>(xb + wb) - 254);
 }
 
 template <int MT>

@@ -1,0 +1,60 @@
+"""The block-scaled FP8 layer where its numbers leave the ordinary range, and
+where a lost token or a lost thread would not show in a sum's tolerance.
+
+What can be exact is compared exactly; other bounds are derived at their test."""
+
+import numpy as np
+import pytest
+
+import oracle
+from parity import bf16_to_numpy
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import rotation_bit_ptq_b200 as rbq  # noqa: E402
+
+F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert rbq.device_error() == 0
+
+
+def _codes(values):
+    return torch.from_numpy(np.asarray(values, dtype=np.float32)).cuda().to(F8)
+
+
+def _scales(bytes_):
+    return torch.from_numpy(np.asarray(bytes_).astype(np.uint8)).cuda().view(E8)
+
+
+# ---- far scales -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 9, 300, 4100])
+def test_sums_of_large_codes_under_far_scales(M):
+    """Sixteen products 448 * 448 under scales whose own product may be anything: a token
+    has the same result alone and beside tokens of other scales, and a sum
+    overflows only where the result does.  16 * 448^2 = 49 * 2^16 is a BF16 number, so
+    every result in its normal range is exact."""
+    eb = np.array([10, 127, 244, 100, 247, 20, 150])
+    K, N = 128, 128 * len(eb)
+    q = np.zeros((M, K))
+    q[:, 16:32] = 448.0
+    w = np.zeros((N, K))
+    w[:, 16:32] = 448.0
+    e = eb[np.arange(M) % len(eb)]
+    y = bf16_to_numpy(rbq.qlinear_fp8(_codes(q), _scales(e[:, None]), _codes(w), _scales(eb[:, None])))
+    exp = e[:, None] + eb[np.arange(N) // 128][None, :] - 254
+    ref = np.ldexp(49.0 * 2 ** 16, exp)
+    sure = ref >= 2.0 ** -126
+    fits = ref <= float(torch.finfo(torch.bfloat16).max)
+    assert (sure & fits).any()
+    assert np.array_equal(y[sure & fits], ref[sure & fits])
+    assert np.all(np.isinf(y[ref >= 2.0 ** 128])) and np.all(np.abs(y[~sure]) <= 2.0 ** -126)
