@@ -468,7 +468,9 @@ int quantize_rotated(const void* Xrot, int dtype, int T, int d, int bits, void* 
  *   s = the smallest power of two with amax / s <= 448, at least 2^-117,
  * amax the largest finite |value| of the block, and round value / s to
  * nearest even.  NaN and infinities become NaN codes (0x7F / 0xFF) and do not
- * count for amax.  Every decoded value is exact in BF16.
+ * count for amax.  Every decoded value is exact in BF16, but for the codes of
+ * |value| >= 248 * 2^120 = 3.296e38: they hold 2^128, which qlinear_fp8_wgrad
+ * takes as infinity.
  *
  * The first call of an entry point on a device sets its kernels up and may
  * allocate the library's device error word: make it before a stream capture.

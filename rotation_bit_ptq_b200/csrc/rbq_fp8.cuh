@@ -12,7 +12,9 @@
 // kernels feed their MMAs.  E4M3 is a floating-point format: up to the
 // binade of its subnormals the larger step between scales costs no accuracy.
 // The floor 2^-117 keeps every decoded value (down to 2^-9 s) a normal BF16
-// number; a block of zeros gets it.
+// number; a block of zeros gets it.  At the other end, |x| of 248 * 2^120
+// (3.296e38) and more rounds to the code of 2^128, which BF16 and fp32 hold as
+// infinity.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -340,7 +340,10 @@ __global__ void __launch_bounds__(kRowThreads)
     const uint4 c = *reinterpret_cast<const uint4*>(xcodes + p.off);
     w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
   }
-  const f2 xs = both(p.n ? scale_value(xscales[p.so]) : 0.f);
+  // From 2^-9 * 2^100 on the slope is 0 or 1: larger scales count as 2^100, under
+  // which no code overflows (256 * 2^120, of an |x| above 3.29e38, does).
+  const uint32_t xb = p.n ? xscales[p.so] : kMinScale;
+  const f2 xs = both(scale_value(xb == 255u ? xb : min(xb, 227u)));
 #pragma unroll
   for (int i = 0; i < kVals / 2; ++i) {
     const float2 v = decode2(w[i / 2] >> (16 * (i & 1)));

@@ -58,3 +58,35 @@ def test_sums_of_large_codes_under_far_scales(M):
     assert (sure & fits).any()
     assert np.array_equal(y[sure & fits], ref[sure & fits])
     assert np.all(np.isinf(y[ref >= 2.0 ** 128])) and np.all(np.abs(y[~sure]) <= 2.0 ** -126)
+
+
+# ---- the GELU's slope at the ends -------------------------------------------------------
+
+@pytest.mark.parametrize("quantize", [False, True])
+def test_gelu_backward_of_the_largest_values(quantize):
+    """Where the checkpoint holds 2^128 (a code 256 under 2^120) the slope is 1 or 0
+    as anywhere far out: dX is dH or 0, not NaN."""
+    v = np.array([3.4e38, -3.4e38, 3.3e38, -3.3e38, 3.2e38, -3.2e38, 1e30, -1e30], dtype=np.float32)
+    x = np.zeros((len(v), 128), dtype=np.float32)
+    x[:, 3] = v
+    xq, xs = rbq.quantize_fp8(torch.from_numpy(x).cuda())
+    dh = torch.full((len(v), 128), 0.75, device="cuda").bfloat16()
+    out = rbq.gelu_backward_fp8(dh, xq, xs, quantize=quantize)
+    dx = bf16_to_numpy(out[0] if quantize else out)
+    assert np.array_equal(dx[:, 3], np.where(v > 0, 0.75, 0.0))
+    assert np.all(np.delete(dx, 3, 1) == 0.375)
+
+
+def test_gelu_backward_under_every_scale():
+    """Zero, the smallest, 1 and the largest code of both signs under all 256 scale bytes."""
+    codes = np.array([0.0, 2.0 ** -9, 1.0, 448.0, -(2.0 ** -9), -1.0, -448.0, 0.0] * 16)
+    q = _codes(np.tile(codes, (256, 1)))
+    dx = bf16_to_numpy(rbq.gelu_backward_fp8(torch.ones(256, 128, device="cuda").bfloat16(), q,
+                                             _scales(np.arange(256)[:, None])))
+    assert np.isnan(dx[255]).all()
+    x = np.ldexp(codes[None, :], np.arange(255)[:, None] - 127)
+    ref = oracle.gelu_slope(np.clip(x, -1e30, 1e30))          # there the slope is 0 or 1 to 64 bits
+    # half a BF16 step; the slope's own error, 4e-7 (1 + |x|) while it is neither 0 nor 1
+    assert np.all(np.abs(dx[:255] - ref) <= 2.0 ** -8 * np.abs(ref) + 4e-7 * (1 + np.minimum(np.abs(x), 14)))
+    far = np.abs(x) >= 14
+    assert np.array_equal(dx[:255][far], (x[far] > 0).astype(np.float64))
