@@ -285,6 +285,14 @@ def gelu_backward_fp8(dH, x_codes, x_scale, quantize=False, out=None, stream=Non
 _linear = None
 
 
+def _rows(t):
+    """The matrix [-1, t.shape[-1]], contiguous and on a 16-byte boundary.  A
+    gradient may come as a view that begins anywhere (that of one part of a
+    concatenation does), a weight as a piece of a flat buffer."""
+    t = t.reshape(-1, t.shape[-1]).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _linear_function():
     """The autograd function behind linear_fp8 (defined on first use: importing
     the package does not import torch)."""
@@ -298,11 +306,11 @@ def _linear_function():
         @staticmethod
         def forward(ctx, X, W, activation):
             need_x, need_w = ctx.needs_input_grad[:2]
-            x2 = X.reshape(-1, X.shape[-1]).contiguous()
+            x2 = _rows(X)
             gelu = _ACTS[activation] == RBQ_ACT_GELU
             keep_x = gelu and need_x
             aq, asc, *ck = quantize_fp8(x2, activation=activation, checkpoint=keep_x)
-            wq, wsc, *wt = quantize_weights_fp8(W.contiguous(), transposed=need_x)
+            wq, wsc, *wt = quantize_weights_fp8(_rows(W), transposed=need_x)
             y = qlinear_fp8(aq, asc, wq, wsc)
             ctx.save_for_backward(*((aq, asc) if need_w else (None, None)), *(wt or (None, None)),
                                   *(ck or (None, None)))
@@ -313,7 +321,7 @@ def _linear_function():
         @once_differentiable
         def backward(ctx, dY):
             aq, asc, wt, wt_sc, xq, xsc = ctx.saved_tensors
-            dy2 = dY.reshape(-1, dY.shape[-1]).contiguous()
+            dy2 = _rows(dY)
             dX = dW = None
             if ctx.needs_input_grad[0]:
                 dX = qlinear_fp8(*quantize_fp8(dy2), wt, wt_sc)

@@ -90,3 +90,32 @@ def test_gelu_backward_under_every_scale():
     assert np.all(np.abs(dx[:255] - ref) <= 2.0 ** -8 * np.abs(ref) + 4e-7 * (1 + np.minimum(np.abs(x), 14)))
     far = np.abs(x) >= 14
     assert np.array_equal(dx[:255][far], (x[far] > 0).astype(np.float64))
+
+
+# ---- operands and gradients that begin anywhere -----------------------------------------
+
+def test_linear_takes_views_at_any_address():
+    """X and W inside flat buffers, and a gradient that is a view into the gradient
+    of a concatenation: none begins on a 16-byte boundary."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T, K, N = 40, 64, 32
+    x = torch.randn(T * K + 3, device="cuda", generator=g).bfloat16()
+    w = torch.randn(N * K + 1, device="cuda", generator=g)
+    head = torch.randn(5, device="cuda", generator=g).bfloat16().requires_grad_()
+    up = torch.randn(5 + T * N, device="cuda", generator=g).bfloat16()
+
+    def step(X, W):
+        y = rbq.linear_fp8(X, W, activation="gelu")
+        torch.cat([head, y.flatten()]).backward(up)
+        return y
+
+    xv, wv = x[3:].view(T, K).detach().requires_grad_(), w[1:].view(N, K).detach().requires_grad_()
+    assert xv.data_ptr() % 16 and wv.data_ptr() % 16 and up[5:].data_ptr() % 16
+    y = step(xv, wv)
+    xc, wc = xv.detach().clone().requires_grad_(), wv.detach().clone().requires_grad_()
+    assert torch.equal(y, step(xc, wc))
+    assert torch.equal(xv.grad, xc.grad) and torch.equal(wv.grad, wc.grad)
+    dy = up[5:].clone().view(T, N)
+    y2 = rbq.linear_fp8(xc, wc, activation="gelu")
+    gx, gw = torch.autograd.grad(y2, (xc, wc), dy)
+    assert torch.equal(gx, xc.grad) and torch.equal(gw, wc.grad)
