@@ -9,6 +9,11 @@
 // fails, and the binding then makes it in Python, where the errors are worded.
 // No error is decided here and no exception leaves a function.
 //
+// The interpreter lock is released while results are allocated and kernels
+// launched, as ctypes and torch's own operators do: a launch waits when the
+// stream's queue is full, and an allocation may.  What is used meanwhile are
+// tensors of the call's own, not the arguments' objects.
+//
 // The entry points of librbq.so are handed over by bind(), so that the two
 // libraries do not depend on one another.
 
@@ -35,28 +40,40 @@ decltype(&gelu_backward_fp8) p_gelu = nullptr;
 constexpr int64_t kBlock = 128, kMost = INT32_MAX;
 int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
-// A matrix as every function wants it; nullptr for anything else.
-const at::Tensor* matrix(PyObject* o) {
-  if (!THPVariable_CheckExact(o)) return nullptr;
+// Without the interpreter lock, to the end of the scope.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
+// A matrix as every function wants it, owned; undefined for anything else.
+at::Tensor matrix(PyObject* o) {
+  if (!THPVariable_CheckExact(o)) return {};
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.defined() || !t.is_cuda() || t.dim() != 2 || !t.is_contiguous()) return nullptr;
-  return t.size(0) <= kMost && t.size(1) <= kMost ? &t : nullptr;
+  if (!t.defined() || !t.is_cuda() || t.dim() != 2 || !t.is_contiguous()) return {};
+  return t.size(0) <= kMost && t.size(1) <= kMost ? t : at::Tensor();
 }
 bool width(int64_t n, int64_t step = 16) { return n > 0 && n % step == 0; }
 
 // Codes [n, d] and their scales, one for `rows` rows of 128 values.
 struct Codes {
-  const at::Tensor *codes = nullptr, *scale = nullptr;
+  at::Tensor codes, scale;
   int64_t n = 0, d = 0;
   bool read(PyObject* c, PyObject* s, int64_t rows) {
     codes = matrix(c);
     scale = matrix(s);
-    if (!codes || !scale || codes->scalar_type() != at::kFloat8_e4m3fn ||
-        scale->scalar_type() != at::kFloat8_e8m0fnu || codes->get_device() != scale->get_device())
+    if (!codes.defined() || !scale.defined() || codes.scalar_type() != at::kFloat8_e4m3fn ||
+        scale.scalar_type() != at::kFloat8_e8m0fnu || codes.get_device() != scale.get_device())
       return false;
-    n = codes->size(0);
-    d = codes->size(1);
-    return width(d) && scale->size(0) == (rows == 1 ? n : blocks(n)) && scale->size(1) == blocks(d);
+    n = codes.size(0);
+    d = codes.size(1);
+    return width(d) && scale.size(0) == (rows == 1 ? n : blocks(n)) && scale.size(1) == blocks(d);
   }
 };
 
@@ -114,21 +131,27 @@ PyObject* attempt(F body) {
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attempt([&]() -> PyObject* {
     if (n != 3 || !p_quantize) return nullptr;
-    const at::Tensor* x = matrix(a[0]);
+    const at::Tensor x = matrix(a[0]);
     const long act = PyLong_AsLong(a[1]);
     const bool ck = a[2] == Py_True;
-    if (!x || dtype_code(*x) < 0 || !width(x->size(1)) || (ck && act == RBQ_ACT_NONE)) return nullptr;
+    if (!x.defined() || dtype_code(x) < 0 || !width(x.size(1)) || (ck && act == RBQ_ACT_NONE)) return nullptr;
     void* st;
-    if (!stream_of(*x, &st)) return nullptr;
-    const int64_t T = x->size(0), d = x->size(1);
-    at::Tensor codes = make_codes(T, d, *x), scale = make_scale(T, blocks(d), *x), xc, xs;
-    if (ck) {
-      xc = make_codes(T, d, *x);
-      xs = make_scale(T, blocks(d), *x);
+    if (!stream_of(x, &st)) return nullptr;
+    const int64_t T = x.size(0), d = x.size(1);
+    at::Tensor codes, scale, xc, xs;
+    int rc;
+    {
+      Unlocked unlocked;
+      codes = make_codes(T, d, x);
+      scale = make_scale(T, blocks(d), x);
+      if (ck) {
+        xc = make_codes(T, d, x);
+        xs = make_scale(T, blocks(d), x);
+      }
+      rc = p_quantize(x.data_ptr(), dtype_code(x), static_cast<int>(T), static_cast<int>(d), static_cast<int>(act),
+                      ptr(codes), ptr(scale), ck ? ptr(xc) : nullptr, ck ? ptr(xs) : nullptr, st);
     }
-    if (p_quantize(x->data_ptr(), dtype_code(*x), static_cast<int>(T), static_cast<int>(d), static_cast<int>(act),
-                   ptr(codes), ptr(scale), ck ? ptr(xc) : nullptr, ck ? ptr(xs) : nullptr, st) != RBQ_OK)
-      return nullptr;
+    if (rc != RBQ_OK) return nullptr;
     return ck ? tuple({codes, scale, xc, xs}) : tuple({codes, scale});
   });
 }
@@ -137,20 +160,26 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attempt([&]() -> PyObject* {
     if (n != 2 || !p_weights) return nullptr;
-    const at::Tensor* w = matrix(a[0]);
+    const at::Tensor w = matrix(a[0]);
     const bool tr = a[1] == Py_True;
-    if (!w || dtype_code(*w) < 0 || !width(w->size(1)) || (tr && !width(w->size(0)))) return nullptr;
+    if (!w.defined() || dtype_code(w) < 0 || !width(w.size(1)) || (tr && !width(w.size(0)))) return nullptr;
     void* st;
-    if (!stream_of(*w, &st)) return nullptr;
-    const int64_t N = w->size(0), K = w->size(1);
-    at::Tensor codes = make_codes(N, K, *w), scale = make_scale(blocks(N), blocks(K), *w), ct, sct;
-    if (tr) {
-      ct = make_codes(K, N, *w);
-      sct = make_scale(blocks(K), blocks(N), *w);
+    if (!stream_of(w, &st)) return nullptr;
+    const int64_t N = w.size(0), K = w.size(1);
+    at::Tensor codes, scale, ct, sct;
+    int rc;
+    {
+      Unlocked unlocked;
+      codes = make_codes(N, K, w);
+      scale = make_scale(blocks(N), blocks(K), w);
+      if (tr) {
+        ct = make_codes(K, N, w);
+        sct = make_scale(blocks(K), blocks(N), w);
+      }
+      rc = p_weights(w.data_ptr(), dtype_code(w), static_cast<int>(N), static_cast<int>(K), ptr(codes), ptr(scale),
+                     tr ? ptr(ct) : nullptr, tr ? ptr(sct) : nullptr, st);
     }
-    if (p_weights(w->data_ptr(), dtype_code(*w), static_cast<int>(N), static_cast<int>(K), ptr(codes), ptr(scale),
-                  tr ? ptr(ct) : nullptr, tr ? ptr(sct) : nullptr, st) != RBQ_OK)
-      return nullptr;
+    if (rc != RBQ_OK) return nullptr;
     return tr ? tuple({codes, scale, ct, sct}) : tuple({codes, scale});
   });
 }
@@ -160,15 +189,19 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attempt([&]() -> PyObject* {
     Codes x, w;
     if (n != 4 || !p_linear || !x.read(a[0], a[1], 1) || !w.read(a[2], a[3], kBlock) || x.d != w.d ||
-        x.codes->get_device() != w.codes->get_device())
+        x.codes.get_device() != w.codes.get_device())
       return nullptr;
     void* st;
-    if (!stream_of(*x.codes, &st)) return nullptr;
-    at::Tensor y = make(x.n, w.n, at::kBFloat16, *x.codes);
-    if (p_linear(ptr(*x.codes), ptr(*x.scale), ptr(*w.codes), ptr(*w.scale), static_cast<int>(x.n),
-                 static_cast<int>(w.n), static_cast<int>(x.d), ptr<uint16_t>(y), st) != RBQ_OK)
-      return nullptr;
-    return THPVariable_Wrap(y);
+    if (!stream_of(x.codes, &st)) return nullptr;
+    at::Tensor y;
+    int rc;
+    {
+      Unlocked unlocked;
+      y = make(x.n, w.n, at::kBFloat16, x.codes);
+      rc = p_linear(ptr(x.codes), ptr(x.scale), ptr(w.codes), ptr(w.scale), static_cast<int>(x.n),
+                    static_cast<int>(w.n), static_cast<int>(x.d), ptr<uint16_t>(y), st);
+    }
+    return rc == RBQ_OK ? THPVariable_Wrap(y) : nullptr;
   });
 }
 
@@ -176,20 +209,23 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attempt([&]() -> PyObject* {
     if (n != 4 || !p_wgrad) return nullptr;
-    const at::Tensor* dy = matrix(a[0]);
+    const at::Tensor dy = matrix(a[0]);
     Codes x;
-    if (!dy || dy->scalar_type() != at::kBFloat16 || !x.read(a[1], a[2], 1) || dy->size(0) != x.n ||
-        !width(dy->size(1), 8) || dy->get_device() != x.codes->get_device())
+    if (!dy.defined() || dy.scalar_type() != at::kBFloat16 || !x.read(a[1], a[2], 1) || dy.size(0) != x.n ||
+        !width(dy.size(1), 8) || dy.get_device() != x.codes.get_device())
       return nullptr;
     void* st;
-    if (!stream_of(*dy, &st)) return nullptr;
+    if (!stream_of(dy, &st)) return nullptr;
     const bool f32 = a[3] == Py_True;
-    at::Tensor dw = make(dy->size(1), x.d, f32 ? at::kFloat : at::kBFloat16, *dy);
-    if (p_wgrad(ptr<uint16_t>(*dy), ptr(*x.codes), ptr(*x.scale), static_cast<int>(x.n),
-                static_cast<int>(dy->size(1)), static_cast<int>(x.d), dw.data_ptr(), f32 ? RBQ_F32 : RBQ_BF16,
-                st) != RBQ_OK)
-      return nullptr;
-    return THPVariable_Wrap(dw);
+    at::Tensor dw;
+    int rc;
+    {
+      Unlocked unlocked;
+      dw = make(dy.size(1), x.d, f32 ? at::kFloat : at::kBFloat16, dy);
+      rc = p_wgrad(ptr<uint16_t>(dy), ptr(x.codes), ptr(x.scale), static_cast<int>(x.n),
+                   static_cast<int>(dy.size(1)), static_cast<int>(x.d), dw.data_ptr(), f32 ? RBQ_F32 : RBQ_BF16, st);
+    }
+    return rc == RBQ_OK ? THPVariable_Wrap(dw) : nullptr;
   });
 }
 
@@ -197,22 +233,27 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* gelu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attempt([&]() -> PyObject* {
     if (n != 4 || !p_gelu) return nullptr;
-    const at::Tensor* dh = matrix(a[0]);
+    const at::Tensor dh = matrix(a[0]);
     Codes x;
-    if (!dh || dh->scalar_type() != at::kBFloat16 || !x.read(a[1], a[2], 1) || dh->size(0) != x.n ||
-        dh->size(1) != x.d || dh->get_device() != x.codes->get_device())
+    if (!dh.defined() || dh.scalar_type() != at::kBFloat16 || !x.read(a[1], a[2], 1) || dh.size(0) != x.n ||
+        dh.size(1) != x.d || dh.get_device() != x.codes.get_device())
       return nullptr;
     void* st;
-    if (!stream_of(*dh, &st)) return nullptr;
+    if (!stream_of(dh, &st)) return nullptr;
     const bool quant = a[3] == Py_True;
-    at::Tensor dx = make(x.n, x.d, at::kBFloat16, *dh), codes, scale;
-    if (quant) {
-      codes = make_codes(x.n, x.d, *dh);
-      scale = make_scale(x.n, blocks(x.d), *dh);
+    at::Tensor dx, codes, scale;
+    int rc;
+    {
+      Unlocked unlocked;
+      dx = make(x.n, x.d, at::kBFloat16, dh);
+      if (quant) {
+        codes = make_codes(x.n, x.d, dh);
+        scale = make_scale(x.n, blocks(x.d), dh);
+      }
+      rc = p_gelu(ptr<uint16_t>(dh), ptr(x.codes), ptr(x.scale), static_cast<int>(x.n), static_cast<int>(x.d),
+                  ptr<uint16_t>(dx), quant ? ptr(codes) : nullptr, quant ? ptr(scale) : nullptr, st);
     }
-    if (p_gelu(ptr<uint16_t>(*dh), ptr(*x.codes), ptr(*x.scale), static_cast<int>(x.n), static_cast<int>(x.d),
-               ptr<uint16_t>(dx), quant ? ptr(codes) : nullptr, quant ? ptr(scale) : nullptr, st) != RBQ_OK)
-      return nullptr;
+    if (rc != RBQ_OK) return nullptr;
     return quant ? tuple({dx, codes, scale}) : THPVariable_Wrap(dx);
   });
 }

@@ -119,3 +119,59 @@ def test_linear_takes_views_at_any_address():
     y2 = rbq.linear_fp8(xc, wc, activation="gelu")
     gx, gw = torch.autograd.grad(y2, (xc, wc), dy)
     assert torch.equal(gx, xc.grad) and torch.equal(gw, wc.grad)
+
+
+# ---- other threads ------------------------------------------------------------------------
+
+def test_native_calls_release_the_interpreter_lock():
+    """The entry points are replaced by PyGILState_Check, which takes no arguments and
+    returns 1 if the calling thread holds the lock: the native binding takes that
+    for an error code and answers None, and 0 for success.  Nothing is launched."""
+    import ctypes
+
+    from rotation_bit_ptq_b200 import _fp8
+    native = _fp8._ordinary()
+    x = torch.randn(32, 256, device="cuda").bfloat16()
+    a, w = rbq.quantize_fp8(x), rbq.quantize_weights_fp8(x)
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    native.bind(*[check] * 5)
+    try:
+        got = [native.quantize_fp8(x, 0, False), native.quantize_weights_fp8(x, True), native.qlinear_fp8(*a, *w),
+               native.qlinear_fp8_wgrad(x, *a, False), native.gelu_backward_fp8(x, *a, True)]
+    finally:
+        _fp8._native = None
+        _fp8._ordinary()                                  # binds librbq.so again
+    assert [r is not None for r in got] == [True] * 5
+    assert torch.equal(rbq.quantize_fp8(x)[0].view(torch.uint8), a[0].view(torch.uint8))
+
+
+def test_threads_at_once():
+    """Four threads, each with a stream of its own, get what each gets alone."""
+    import threading
+
+    def work(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn(100 + seed, 400, device="cuda", generator=g).bfloat16()
+        w = (torch.randn(272, 400, device="cuda", generator=g) * 0.1).requires_grad_()
+        out = []
+        for _ in range(20):
+            y = rbq.linear_fp8(x, w, activation="gelu")
+            out.append((y.detach(), *torch.autograd.grad(y, w, torch.ones_like(y))))
+        return out
+
+    ref = [work(s) for s in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[i] = work(i)
+            torch.cuda.current_stream().synchronize()
+
+    ts = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for r, o in zip(ref, got):
+        assert all(torch.equal(p, q) for a, b in zip(r, o) for p, q in zip(a, b))
