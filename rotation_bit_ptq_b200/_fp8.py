@@ -50,10 +50,15 @@ def _ordinary():
     global _native
     if _native is None:
         import torch  # noqa: F401  (loads the libraries _rbq_call.so links)
+
+        from .build import built_for
+        here = built_for()
         try:
             from . import _rbq_call
+            if getattr(_rbq_call, "built_for", None) != here:
+                raise ImportError(f"it was built for {getattr(_rbq_call, 'built_for', 'something else')}")
         except ImportError as e:
-            raise RuntimeError("_rbq_call.so is missing or does not fit this torch: build it with "
+            raise RuntimeError(f"_rbq_call.so is missing or not built for {here}: build it with "
                                "`python -m rotation_bit_ptq_b200.build`") from e
         _rbq_call.bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
             "quantize_fp8", "quantize_weights_fp8", "qlinear_fp8", "qlinear_fp8_wgrad", "gelu_backward_fp8")))

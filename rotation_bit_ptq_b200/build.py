@@ -12,6 +12,7 @@ installed torch.
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -97,16 +98,32 @@ def build(verbose=False, ptxas_info=False, jobs=None, debug=False):
     return lib
 
 
+def built_for():
+    """What _rbq_call.so depends on besides its source: it is compiled against the
+    headers of one torch and one Python, and holds this text."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:       # a torch that was not installed as a package
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
 def build_binding(verbose=False):
-    """Compile csrc/rbq_call.cpp to _rbq_call.so."""
+    """Compile csrc/rbq_call.cpp to _rbq_call.so, if it is older than its source or
+    was built for another torch or Python."""
     src = os.path.join(CSRC, "rbq_call.cpp")
-    if not _stale(BINDING, src, os.path.getmtime(os.path.join(INCLUDE, "rbq.h"))):
-        return BINDING
+    key = built_for()
+    key_file = os.path.join(BUILD, "rbq_call.key")
+    if not _stale(BINDING, src, os.path.getmtime(os.path.join(INCLUDE, "rbq.h"))) and os.path.exists(key_file):
+        with open(key_file) as f:
+            if f.read() == key:
+                return BINDING
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     inc, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           f'-DRBQ_BUILT_FOR="{key}"', "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda_inc, src, "-o", BINDING,
            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -114,6 +131,9 @@ def build_binding(verbose=False):
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode:
         raise RuntimeError("g++ failed on rbq_call.cpp")
+    os.makedirs(BUILD, exist_ok=True)
+    with open(key_file, "w") as f:
+        f.write(key)
     return BINDING
 
 

@@ -289,4 +289,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rbq_call", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rbq_call() { return PyModule_Create(&module); }
+// `built_for`: the torch and the Python whose headers this was compiled against;
+// the binding calls nothing here under any other.
+PyMODINIT_FUNC PyInit__rbq_call() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", RBQ_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

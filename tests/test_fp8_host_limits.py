@@ -2,10 +2,13 @@
 without a GPU."""
 
 import ctypes
+import importlib.metadata
+from types import SimpleNamespace
 
 import pytest
 
 import rotation_bit_ptq_b200 as rbq
+from rotation_bit_ptq_b200 import build
 
 FAKE = ctypes.c_void_p(0x10000)                  # never dereferenced
 BF, NONE, GELU = rbq.RBQ_BF16, rbq.RBQ_ACT_NONE, rbq.RBQ_ACT_GELU
@@ -40,3 +43,44 @@ def test_the_limit_itself_is_allowed(lib):
     assert lib.qlinear_fp8(None, None, None, None, 0, MOST, MOST, None, None) == rbq.RBQ_OK
     assert lib.qlinear_fp8_wgrad(None, None, None, MOST, 0, MOST, None, BF, None) == rbq.RBQ_OK
     assert lib.gelu_backward_fp8(None, None, None, 0, MOST, None, None, None, None) == rbq.RBQ_OK
+
+
+# ---- the native binding's build -----------------------------------------------------
+
+@pytest.fixture
+def compiles(monkeypatch, tmp_path):
+    """build_binding with files of its own and a compiler that only writes the output; the calls made."""
+    calls = []
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_rbq_call.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return calls
+
+
+def test_binding_is_built_again_for_another_torch(compiles, monkeypatch):
+    build.build_binding()
+    build.build_binding()
+    assert len(compiles) == 1                              # up to date
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "9.9.9" if name == "torch" else version(name))
+    build.build_binding()
+    build.build_binding()
+    assert len(compiles) == 2
+
+
+def test_binding_of_another_torch_is_refused(monkeypatch):
+    """A library that loads but was built for another torch, whose objects may be
+    laid out differently, is not called."""
+    from rotation_bit_ptq_b200 import _fp8
+    monkeypatch.setattr(_fp8, "_native", None)
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "9.9.9" if name == "torch" else version(name))
+    with pytest.raises(RuntimeError, match="9.9.9"):
+        _fp8._ordinary()
+    assert _fp8._native is None
