@@ -7,7 +7,7 @@ linked next to this file.  The CUDA runtime is linked statically.
 
 Beside it goes _rbq_call.so, the native part of the Python binding
 (csrc/rbq_call.cpp), compiled by the host compiler against the headers of the
-installed torch.
+installed torch (left out where there is none).
 """
 
 import concurrent.futures
@@ -111,7 +111,12 @@ def built_for():
 
 def build_binding(verbose=False):
     """Compile csrc/rbq_call.cpp to _rbq_call.so, if it is older than its source or
-    was built for another torch or Python."""
+    was built for another torch or Python.  Without torch there is nothing to
+    bind (librbq.so needs none): returns None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        sys.stderr.write("torch is not installed: _rbq_call.so, the native part of the Python binding, is not built\n")
+        return None
     src = os.path.join(CSRC, "rbq_call.cpp")
     key = built_for()
     key_file = os.path.join(BUILD, "rbq_call.key")
@@ -119,7 +124,7 @@ def build_binding(verbose=False):
         with open(key_file) as f:
             if f.read() == key:
                 return BINDING
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = spec.submodule_search_locations[0]
     inc, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden",

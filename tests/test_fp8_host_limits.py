@@ -3,6 +3,7 @@ without a GPU."""
 
 import ctypes
 import importlib.metadata
+import importlib.util
 from types import SimpleNamespace
 
 import pytest
@@ -84,3 +85,11 @@ def test_binding_of_another_torch_is_refused(monkeypatch):
     with pytest.raises(RuntimeError, match="9.9.9"):
         _fp8._ordinary()
     assert _fp8._native is None
+
+
+def test_the_library_is_built_without_torch(compiles, monkeypatch, capsys):
+    """librbq.so needs no torch, so the build ends well where there is none; what is left out is said."""
+    find_spec = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find_spec(name, *a))
+    assert build.build_binding() is None
+    assert compiles == [] and "torch" in capsys.readouterr().err
