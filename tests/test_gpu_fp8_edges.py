@@ -175,3 +175,54 @@ def test_threads_at_once():
         t.join()
     for r, o in zip(ref, got):
         assert all(torch.equal(p, q) for a, b in zip(r, o) for p, q in zip(a, b))
+
+
+# ---- every token and every value counts ---------------------------------------------------
+
+# Sums of small integers: exact in fp32 whatever their order, so that one lost,
+# doubled or misplaced term shows.  (With heavy-tailed operands a few tokens carry
+# the sum, and the others fall within the tolerance of a long sum.)
+
+def _integers(g, n, d, rows, lo, hi):
+    """Codes of integers lo..hi under scales 1, 2 and 4, and the values as fp64 on the GPU."""
+    v = torch.randint(lo, hi + 1, (n, d), device="cuda", generator=g)
+    e = torch.randint(0, 3, (-(-n // rows), -(-d // 128)), device="cuda", generator=g)
+    s = torch.exp2(e.double()).repeat_interleave(rows, 0)[:n].repeat_interleave(128, 1)[:, :d]
+    return v.float().to(F8), (e + 127).to(torch.uint8).view(E8), v.double() * s
+
+
+# One token, the last one alone in its slice of 64, the last one missing from it;
+# narrow and wide tiles, one part and several.
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (63, 264, 272), (64, 264, 272), (65, 264, 272), (3001, 64, 128),
+                                   (4033, 64, 128), (4031, 64, 128), (1561, 520, 400), (1599, 520, 400),
+                                   (6017, 40, 48), (20033, 264, 272), (321, 4096, 4096), (319, 4096, 4096),
+                                   (4097, 4096, 1040), (8001, 1536, 1536), (2047, 2048, 2064)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weight_gradient_counts_every_token(M, N, K, dtype):
+    """Token m's gradient is one entry of size 1 to 3 in column m % N, its codes are 1 to 3: without it
+    row m % N differs everywhere.  The sums stay below 2^24."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    aq, asc, a = _integers(g, M, K, 1, 1, 3)
+    rows = torch.arange(M, device="cuda")
+    up = torch.randint(1, 4, (M,), device="cuda", generator=g).double()
+    dy = torch.zeros(M, N, device="cuda", dtype=torch.bfloat16)
+    dy[rows, rows % N] = up.bfloat16()
+    ref = torch.zeros(N, K, device="cuda", dtype=torch.float64).index_add_(0, rows % N, a * up[:, None])
+    dW = rbq.qlinear_fp8_wgrad(dy, aq, asc, dtype=dtype)
+    assert float(ref.max()) < 2 ** 24
+    assert torch.equal(dW, ref.to(dtype))
+
+
+# Every kernel: dot products of one to four tokens, 16 to 256 tokens to a tile
+# with K in one part and in several, and CTA pairs; whole and short last blocks of K.
+@pytest.mark.parametrize("M,N,K", [(1, 1001, 2064), (2, 130, 144), (3, 136, 4112), (4, 1000, 2048), (15, 300, 1040),
+                                   (9, 1000, 40000), (33, 1001, 656), (64, 512, 1536), (100, 520, 1040),
+                                   (255, 500, 1552), (300, 1001, 1552), (513, 2056, 656), (40, 64, 33024),
+                                   (4097, 3001, 272), (4100, 2600, 8960), (2000, 2048, 2064)])
+def test_layer_counts_every_value(M, N, K):
+    """Integers -2 to 2 under scales 1 to 4: the sums (below 2^24) are exact, the result their BF16 rounding."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    aq, asc, a = _integers(g, M, K, 1, -2, 2)
+    wq, wsc, w = _integers(g, N, K, 128, -2, 2)
+    assert 64 * K < 2 ** 24
+    assert torch.equal(rbq.qlinear_fp8(aq, asc, wq, wsc), (a @ w.t()).to(torch.bfloat16))
