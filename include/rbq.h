@@ -480,8 +480,8 @@ int quantize_rotated(const void* Xrot, int dtype, int T, int d, int bits, void* 
  * quantize_fp8 -- codes and scales of the rows of act(X).
  *   X          device [T, d], RBQ_BF16 or RBQ_F32, 16-byte aligned
  *   T, d       rows (0 is a valid no-op); width, a multiple of 16, at most 2^30
- *   activation RBQ_ACT_NONE or RBQ_ACT_GELU (fp32; |error| <= 1e-7 |x|, and
- *              for x in [-7, 0) <= 5e-3 of the value itself)
+ *   activation RBQ_ACT_NONE or RBQ_ACT_GELU (fp32; |error| <= 2.5e-7 |x|,
+ *              and for x in [-7, 0) <= 5e-3 of the value itself)
  *   codes      device uint8 [T, d], 16-byte aligned
  *   scales     device uint8 [T, ceil(d / 128)]
  *   x_codes, x_scales  with RBQ_ACT_GELU: the same of X itself, an 8-bit

@@ -216,10 +216,13 @@ __device__ __forceinline__ void encode(const V& x, float inv, uint32_t (&w)[V::k
 // ---- the GELU --------------------------------------------------------------------
 // Phi(-z) = 2^Q(z), z = |x|: Q is a polynomial of degree 8, fitted here to
 // log2 Phi(-z) on [0, 7] by iteratively reweighted least squares so that the
-// largest of |error| / max(Phi(-z), 1e-5) is least.  Evaluated in fp32,
-// |error of Phi| <= 8e-8 everywhere, and 9e-4 of Phi(-z) itself to z = 5, 4e-3
-// to z = 7 (an E4M3 code's half step is 6e-2); beyond, it falls below 2e-12 and
-// on to 0.  One exponential and no reciprocal: with erf's usual rational
+// largest of |error| / max(Phi(-z), 1e-5) is least.  With q evaluated in fp32
+// and an exact exponential, |error of Phi| <= 8e-8 everywhere, and 9e-4 of
+// Phi(-z) itself to z = 5, 4.2e-3 to z = 7 (an E4M3 code's half step is 6e-2);
+// beyond, it falls below 2e-12 and on to 0.  ex2.approx adds 2^-22 of Phi(-z),
+// the last FMA of the GELU 2^-24 of the result: in all at most 2.2e-7 |x| for x
+// Phi(x), and with the second exponential 3.3e-7 for its slope while |x| <= 16.
+// One exponential and no reciprocal: with erf's usual rational
 // approximation the kernel was bound by its instructions (38 a value).
 //
 // Everything works on n = -|x| (so the odd coefficients' signs are turned),

@@ -226,3 +226,47 @@ def test_layer_counts_every_value(M, N, K):
     wq, wsc, w = _integers(g, N, K, 128, -2, 2)
     assert 64 * K < 2 ** 24
     assert torch.equal(rbq.qlinear_fp8(aq, asc, wq, wsc), (a @ w.t()).to(torch.bfloat16))
+
+
+# ---- the GELU's own error ---------------------------------------------------------------
+
+def _gelu_preimage(b, lo, hi):
+    """x in [lo, hi] with x Phi(x) = b, by bisection in 64 bits (monotone there)."""
+    lo, hi = np.full_like(b, lo), np.full_like(b, hi)
+    up = oracle.gelu(hi) > oracle.gelu(lo)
+    for _ in range(100):
+        mid = 0.5 * (lo + hi)
+        left = (oracle.gelu(mid) < b) == up
+        lo, hi = np.where(left, mid, lo), np.where(left, hi, mid)
+    return 0.5 * (lo + hi)
+
+
+@pytest.mark.parametrize("j", range(-6, 6))
+def test_gelu_beside_every_border_of_the_codes(j):
+    """The stated |error| <= 2.5e-7 |x| decides the code of an x whose GELU lies further than
+    that from the border of two codes.  Such x are taken as close to the borders as fp32
+    lets them, on both sides, and their codes compared with the exact ones.
+
+    The bound: h = max(x, 0) - |x| t with t = 2^q.  The polynomial, its fp32
+    evaluation included, is off by 8e-8 of Phi(-|x|) (the maximum over [0, 16], taken in 64 bits
+    with every FMA rounded); ex2.approx by 2^-22 t, t <= 1/2; the last FMA by
+    2^-24 |h|.  Over [0, 16] the sum is at most 2.2e-7 |x|."""
+    bound, s = 2.5e-7, 2.0 ** j
+    codes = torch.arange(0x7F, dtype=torch.uint8).view(F8).double().numpy()        # all that are >= 0
+    borders = 0.5 * (codes[:-1] + codes[1:]) * s
+    below = -borders[borders < 0.169]                  # the GELU's least value is -0.1700, at -0.752
+    x0 = np.concatenate([_gelu_preimage(borders, 0.0, 1e6), _gelu_preimage(below, -0.75, 0.0),
+                         _gelu_preimage(below, -6.0, -0.76)])
+    step = bound * np.abs(x0) / np.maximum(np.abs(oracle.gelu_slope(x0)), 1e-3)
+    x = np.concatenate([x0 + k * step for k in (1.1, -1.1, 2.0, -2.0)]).astype(np.float32)
+    h = oracle.gelu(x.astype(np.float64))
+    top = np.float32(440 * s)                          # in every block: it fixes the scale at s
+    away = np.min(np.abs(h[:, None] - np.concatenate([-borders, borders])[None, :]), axis=1)
+    x = x[(away > bound * np.abs(x)) & (np.abs(h) < top)]
+    assert len(x) > 200
+    x = np.pad(x, (0, -len(x) % 127)).reshape(-1, 127)
+    x = np.concatenate([x, np.full((len(x), 1), top)], 1)
+    q, sc = rbq.quantize_fp8(torch.from_numpy(x).cuda(), activation="gelu")
+    rq, re = oracle.fp8_encode(oracle.gelu(x.astype(np.float64)))
+    assert np.all(re == j) and np.all(sc.view(torch.uint8).cpu().numpy() == 127 + j)
+    assert np.array_equal(q.double().cpu().numpy(), rq)
