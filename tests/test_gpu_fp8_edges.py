@@ -270,3 +270,82 @@ def test_gelu_beside_every_border_of_the_codes(j):
     rq, re = oracle.fp8_encode(oracle.gelu(x.astype(np.float64)))
     assert np.all(re == j) and np.all(sc.view(torch.uint8).cpu().numpy() == 127 + j)
     assert np.array_equal(q.double().cpu().numpy(), rq)
+
+
+# ---- the two ways a call is made ---------------------------------------------------------
+
+def _calls():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(64, 256, device="cuda", generator=g)
+    flat = torch.randn(64 * 256 + 4, device="cuda", generator=g)
+    h = x.bfloat16()
+    q, s = rbq.quantize_fp8(x)
+    w, ws = rbq.quantize_weights_fp8(x[:48].contiguous())
+    dy = torch.randn(64, 48, device="cuda", generator=g).bfloat16()
+    q0, s0, h0 = q[:0], s[:0], h[:0]
+    byte = torch.zeros(64 * 256 + 1, dtype=torch.uint8, device="cuda")
+    odd = byte[1:].view(F8).view(64, 256)
+    inputs = (x, h, x.half(), x.double(), x.t(), x[:, :128], x[0], x[:40], x[:, :40].contiguous(), x[:, :0], h0, x.cpu(),
+              flat[4:].view(64, 256), flat[1:-3].view(64, 256), x.view(1, 64, 256), torch.nn.Parameter(x), None, [1.0])
+    for t in inputs:
+        for kw in ({}, {"activation": "gelu"}, {"activation": "gelu", "checkpoint": True}, {"checkpoint": True},
+                   {"activation": "none"}, {"activation": "relu"}):
+            yield rbq.quantize_fp8, (t,), kw
+        for kw in ({}, {"transposed": True}, {"transposed": 1}):
+            yield rbq.quantize_weights_fp8, (t,), kw
+    pairs = ((q, s), (w, ws), (q0, s0), (q, s[:32]), (q, s[:, :1]), (q[:, :128].contiguous(), s[:, :1].contiguous()),
+             (q.view(torch.uint8), s), (q, s.view(torch.uint8)), (q, s.float()), (q.cpu(), s.cpu()), (odd, s), (q.t(), s),
+             (q[0], s[0]), (s, q), (None, s), (q, None))
+    for a in pairs:
+        for b in pairs:
+            yield rbq.qlinear_fp8, (*a, *b), {}
+        for t in (dy, h, dy.float(), dy[:32], dy[:, :12].contiguous(), dy.t(), dy[:0], dy[:, :0], h0, dy.cpu(), None):
+            for kw in ({}, {"dtype": torch.float32}, {"dtype": torch.float16}):
+                yield rbq.qlinear_fp8_wgrad, (t, *a), kw
+            for kw in ({}, {"quantize": True}):
+                yield rbq.gelu_backward_fp8, (t, *a), kw
+
+
+def test_native_and_python_calls_accept_the_same(monkeypatch):
+    """Whatever one way of making a call takes, refuses or answers, the other does."""
+    from types import SimpleNamespace
+
+    from rotation_bit_ptq_b200 import _fp8
+
+    def outcome(f, args, kw):
+        try:
+            r = f(*args, **kw)
+        except Exception as e:
+            return type(e), None
+        return None, r if isinstance(r, tuple) else (r,)
+
+    calls = list(_calls())
+    first = [outcome(*c) for c in calls]
+    native = _fp8._ordinary()
+    made = []
+
+    def noted(name):
+        def f(*args):
+            r = getattr(native, name)(*args)
+            made.append(r is not None)
+            return r
+        return f
+
+    names = ("quantize_fp8", "quantize_weights_fp8", "qlinear_fp8", "qlinear_fp8_wgrad", "gelu_backward_fp8")
+    monkeypatch.setattr(_fp8, "_native", SimpleNamespace(**{n: noted(n) for n in names}))
+    natively = []
+    for c in calls:
+        made.clear()
+        outcome(*c)
+        natively.append(any(made))
+    monkeypatch.setattr(_fp8, "_native", SimpleNamespace(**{n: lambda *a: None for n in names}))
+    second = [outcome(*c) for c in calls]
+    assert 50 < sum(natively) < len(calls) // 2
+    for (e1, r1), (e2, r2), c, by in zip(first, second, calls, natively):
+        what = (c[0].__name__, [getattr(t, "shape", t) for t in c[1]], c[2])
+        assert e1 is e2, (*what, e1, e2)
+        # (those without a row or a column may be left to Python)
+        assert by == (e2 is None) or not all(t.numel() for t in c[1]), what
+        if r1 is not None:
+            assert len(r1) == len(r2) and all(a.dtype == b.dtype and a.shape == b.shape for a, b in zip(r1, r2)), what
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(r1, r2) if a.numel()), what
