@@ -529,8 +529,10 @@ int qlinear_fp8(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* 
  *   M, N, K            at most 2^30
  *   dW                 device [N, K], `dtype` RBQ_BF16 or RBQ_F32, 16-byte
  *                      aligned; overwritten (zeros when M is 0)
- * Workspace from a stream-ordered memory pool: M*K*2 bytes, and 4*N*K for each
- * part when the tokens are split.
+ * Workspace from the library's stream-ordered memory pool, which keeps it for
+ * later calls: M*K*2 bytes but at most 2 GiB (or M*512 bytes if that is more;
+ * beyond it the columns of dW are computed in panels), and 4*N*K for each part
+ * when the tokens of a small dW are split (20 MB at most).
  * Errors: RBQ_EINVAL, RBQ_EALIGN, RBQ_ECUDA.
  */
 int qlinear_fp8_wgrad(const uint16_t* dY, const uint8_t* a_codes, const uint8_t* a_scales, int M, int N, int K,

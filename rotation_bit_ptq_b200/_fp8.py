@@ -233,7 +233,11 @@ def qlinear_fp8(a_codes, a_scale, w_codes, w_scale, out=None, stream=None):
 def qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype=None, out=None, stream=None):
     """dW[n, k] = sum_m dY[m, n] (sa[m, k/128] qa[m, k]), the weight gradient
     of qlinear_fp8 from the bfloat16 dY [M, N] and the codes kept of the
-    layer's input; bfloat16 (the default) or float32 [N, K].  N a multiple of 8."""
+    layer's input; bfloat16 (the default) or float32 [N, K].  N a multiple of 8.
+
+    Takes a workspace of 2 M K bytes, at most 2 GiB (512 M bytes if that is
+    more), from the library's memory pool, which keeps it for later calls: it
+    is not torch's to reuse."""
     import torch
     if out is None and stream is None and dtype in (None, torch.bfloat16, torch.float32):
         dW = (_native or _ordinary()).qlinear_fp8_wgrad(dY, a_codes, a_scale, dtype is torch.float32)
@@ -348,7 +352,10 @@ def linear_fp8(X, W, activation=None):
     Differentiable in X and W.  What the backward pass needs is kept in 8
     bits: the codes of act(X) for dW, of X for the GELU's slope, and of W^T for
     dX (whose other operand, the incoming gradient, is quantised there).  W is
-    quantised in every call.  N and K multiples of 16."""
+    quantised in every call.  N and K multiples of 16.  dX is rounded to bfloat16
+    also for a float32 X, with 'gelu' before and after the slope; dW has W's
+    type.  The backward pass takes qlinear_fp8_wgrad's workspace.  (rotate_act
+    passes no gradient on: X of a layer on rotated inputs is where it ends.)"""
     import torch
     for t, name in ((X, "X"), (W, "W")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:

@@ -10,7 +10,7 @@
 //
 // Two kernels per call (three when the tokens are split):
 // 1. decode_rows_kernel: codes and scales -> BF16 [M, K] in a stream-ordered
-//    workspace.
+//    workspace; above 2 GiB, a panel of columns after the other.
 // 2. wgrad_kernel: persistent, on CTA pairs, tiles of 256 x 256 or 256 x 128
 //    values of dW (cta_group::2), slices of 64 tokens.  Both operands lie with
 //    the token as their row, so they are "MN-major": a TMA box of 64 tokens x
@@ -283,18 +283,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
   }
 }
 
-// Codes and scales -> BF16 values, 16 per thread (K is a multiple of 16); CTA
-// (x, y): 4096 values of each of `rows` rows from row `rows` y on.
+// Codes and scales -> BF16 values [M, cols], 16 per thread (K and cols are
+// multiples of 16); CTA (x, y): 4096 values of each of `rows` rows from row
+// `rows` y on.
 __global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, const uint8_t* scales, int M, int K,
-                                                          int kbs, int rows, uint16_t* out) {
+                                                          int kbs, int cols, int rows, uint16_t* out) {
   griddep_wait();
   griddep_launch_dependents();
   const int col = (blockIdx.x * 256 + threadIdx.x) * 16, row0 = blockIdx.y * rows, row1 = min(M, row0 + rows);
-  if (col >= K) return;
+  if (col >= cols) return;
 #pragma unroll 4
   for (int row = row0; row < row1; ++row) {
-    const long long at = static_cast<long long>(row) * K + col;
-    const uint4 c = *reinterpret_cast<const uint4*>(codes + at);
+    const uint4 c = *reinterpret_cast<const uint4*>(codes + static_cast<long long>(row) * K + col);
     const float s = scale_value(scales[static_cast<long long>(row) * kbs + col / kBlock]);
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t o[8];
@@ -304,18 +304,19 @@ __global__ void __launch_bounds__(256) decode_rows_kernel(const uint8_t* codes, 
       const __nv_bfloat162 h = __floats2bfloat162_rn(v.x * s, v.y * s);      // exact
       o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    st_v8(out + at, o);                     // the workspace and its rows are 32-byte aligned
+    st_v8(out + static_cast<long long>(row) * cols + col, o);       // the workspace and its rows are 32-byte aligned
   }
 }
 
-// out[i] = the sum of the parts: G groups of threads take every G-th part each,
-// in their order, and the groups' sums are added in theirs.  One group where
-// the parts are few; eight where they are many and the gradient small, so that
+// out = the sum of the parts, n4 groups of four values each (cols4 to a row; a
+// row of out is pitch4 long): G groups of threads take every G-th part each, in
+// their order, and the groups' sums are added in theirs.  One group where the
+// parts are few; eight where they are many and the gradient small, so that
 // their loads do not wait for one another (256 x 256 in 27 parts: 9.7 us with
 // one group).
 template <int G>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int nparts, long long n4, void* out,
-                                                        int f32) {
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int nparts, long long n4,
+                                                        unsigned cols4, unsigned pitch4, void* out, int f32) {
   constexpr int kOut = 256 / G;
   __shared__ float4 sums[G > 1 ? 256 : 1];
   griddep_wait();
@@ -341,10 +342,15 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float4* parts, int
     for (int q = 1; q < G; ++q) add(sums[q * kOut + l]);
   }
   if (i >= n4) return;
+  long long o = i;
+  if (cols4 != pitch4) {                    // i < 2^32: the tiles of all parts fit the GPU at once
+    const unsigned r = static_cast<unsigned>(i) / cols4;
+    o = static_cast<long long>(r) * pitch4 + (static_cast<unsigned>(i) - r * cols4);
+  }
   if (f32) {
-    static_cast<float4*>(out)[i] = s;
+    static_cast<float4*>(out)[o] = s;
   } else {
-    static_cast<uint2*>(out)[i] = make_uint2(bf16x2(__float_as_uint(s.x), __float_as_uint(s.y)),
+    static_cast<uint2*>(out)[o] = make_uint2(bf16x2(__float_as_uint(s.x), __float_as_uint(s.y)),
                                              bf16x2(__float_as_uint(s.z), __float_as_uint(s.w)));
   }
 }
@@ -363,11 +369,11 @@ int encode_tokens_map(CUtensorMap* map, const uint16_t* base, int rows, int cols
   return r == CUDA_SUCCESS ? RBQ_OK : RBQ_ECUDA;
 }
 
-// [parts, N, K] of BF16 or fp32, boxes of 32 rows x 128 bytes, 128B swizzle.
-int encode_out_map(CUtensorMap* map, void* base, int parts, int N, int K, bool f32) {
+// [parts, N, K] of BF16 or fp32 with rows `pitch` values apart, boxes of 32 rows x 128 bytes, 128B swizzle.
+int encode_out_map(CUtensorMap* map, void* base, int parts, int N, int K, int pitch, bool f32) {
   auto fn = qfast::encode_fn();
   if (!fn) return RBQ_ECUDA;
-  const cuuint64_t row = (f32 ? 4 : 2) * static_cast<cuuint64_t>(K);
+  const cuuint64_t row = (f32 ? 4 : 2) * static_cast<cuuint64_t>(pitch);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(parts)};
   const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(N)};
   const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
@@ -467,49 +473,50 @@ WPlan make_wplan(int M, int N, int K, int pairs) {
   return best;
 }
 
-int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M, int N, int K, void* dW, bool f32,
-          unsigned int* err, cudaStream_t st) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
+// dW[:, k0 : k0 + cols] (k0 a multiple of kBlock): the values of those columns of x go through the workspace.
+int wgrad_panel(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M, int N, int K, int k0, int cols,
+                void* dW, bool f32, unsigned int* err, int dev, cudaStream_t st) {
+  codes += k0;
+  scales += k0 / kBlock;
+  dW = static_cast<uint8_t*>(dW) + static_cast<size_t>(k0) * (f32 ? 4 : 2);
   const int pairs256 = wgrad_pairs<256>(dev), pairs128 = wgrad_pairs<128>(dev);
   if (pairs256 < 1 || pairs128 < 1) return RBQ_ECUDA;
-  const WPlan plan = make_wplan(M, N, K, pairs256);
+  const WPlan plan = make_wplan(M, N, cols, pairs256);
   const int parts = plan.parts, pairs = plan.BK == 256 ? pairs256 : pairs128;
-  const long long ntiles = ((N + kTileN - 1LL) / kTileN) * ((K + plan.BK - 1LL) / plan.BK);
+  const long long ntiles = ((N + kTileN - 1LL) / kTileN) * ((cols + plan.BK - 1LL) / plan.BK);
   if (ntiles * parts > (1 << 28)) return RBQ_EINVAL;
 
   cudaMemPool_t pool = qfast::workspace_pool(dev);
   if (!pool) return RBQ_ECUDA;
-  const size_t x_bytes = (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256;
-  const size_t part_bytes = parts > 1 ? static_cast<size_t>(parts) * N * K * 4 : 0;
+  const size_t x_bytes = (static_cast<size_t>(M) * cols * 2 + 255) / 256 * 256;
+  const size_t part_bytes = parts > 1 ? static_cast<size_t>(parts) * N * cols * 4 : 0;
   void* ws = nullptr;
-  e = cudaMallocFromPoolAsync(&ws, x_bytes + part_bytes, pool, st);
+  cudaError_t e = cudaMallocFromPoolAsync(&ws, x_bytes + part_bytes, pool, st);
   if (e != cudaSuccess) return cuda_fail(e);
   uint16_t* x = static_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + x_bytes);
 
   // rows per CTA: enough CTAs to fill the GPU, at most 65535 along y
-  const int xs = (K + 4095) / 4096;
+  const int xs = (cols + 4095) / 4096;
   int rows = 1;
   while (rows < 8 && static_cast<long long>(xs) * M / (2 * rows) >= 148 * 8) rows *= 2;
   while ((M + rows - 1) / rows > 65535) rows *= 2;
   int rc = launch(decode_rows_kernel, dim3(xs, (M + rows - 1) / rows, 1), 256, 0, false, st, codes, scales, M, K,
-                  blocks(K), rows, x);
+                  blocks(K), cols, rows, x);
 
   WParams p{};
   p.M = M;
   p.N = N;
-  p.K = K;
+  p.K = cols;
   p.parts = parts;
   p.f32 = parts > 1 || f32;
-  p.order = tiles::tile_order(dev, 2LL * M * N, 2LL * M * K);
+  p.order = tiles::tile_order(dev, 2LL * M * N, 2LL * M * cols);
   p.err = err;
   CUtensorMap mY, mX, mW;
   if (rc == RBQ_OK) rc = encode_tokens_map(&mY, dY, M, N);
-  if (rc == RBQ_OK) rc = encode_tokens_map(&mX, x, M, K);
-  if (rc == RBQ_OK) rc = encode_out_map(&mW, parts > 1 ? static_cast<void*>(part) : dW, parts, N, K, p.f32 != 0);
+  if (rc == RBQ_OK) rc = encode_tokens_map(&mX, x, M, cols);
+  if (rc == RBQ_OK)
+    rc = parts > 1 ? encode_out_map(&mW, part, parts, N, cols, cols, true) : encode_out_map(&mW, dW, 1, N, cols, K, f32);
   if (rc == RBQ_OK) {
     const long long nwork = ntiles * parts;
     const dim3 grid(2 * static_cast<unsigned>(nwork < pairs ? nwork : pairs), 1, 1);
@@ -517,15 +524,38 @@ int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M
                         : launch(wgrad_kernel<128>, grid, kWThreads, kWSmem<128>, true, st, mY, mX, mW, p);
   }
   if (rc == RBQ_OK && parts > 1) {
-    const long long n4 = static_cast<long long>(N) * K / 4, per = parts > 4 ? 32 : 256, grid = (n4 + per - 1) / per;
+    const long long n4 = static_cast<long long>(N) * cols / 4, per = parts > 4 ? 32 : 256, grid = (n4 + per - 1) / per;
     rc = grid > 0x7FFFFFFFll
              ? RBQ_EINVAL
              : launch(parts > 4 ? sum_parts_kernel<8> : sum_parts_kernel<1>, dim3(static_cast<unsigned>(grid), 1, 1),
-                      256, 0, false, st, reinterpret_cast<const float4*>(part), parts, n4, dW, static_cast<int>(f32));
+                      256, 0, false, st, reinterpret_cast<const float4*>(part), parts, n4,
+                      static_cast<unsigned>(cols / 4), static_cast<unsigned>(K / 4), dW, static_cast<int>(f32));
   }
   e = cudaFreeAsync(ws, st);
   if (rc == RBQ_OK && e != cudaSuccess) rc = cuda_fail(e);
   return rc;
+}
+
+// x takes twice the room of its codes in the workspace, and the pool keeps what
+// it once had: so at most 2 GiB of it at a time, a panel of columns after the
+// other.  (131072 x 1024 x 16384 takes 3.9 ms in two panels and 4.1 in one, 70000
+// x 1024 x 16384 2.2 and 2.1: within what the power cap's clock moves them.)
+constexpr long long kPanelBytes = 2ll << 30;
+constexpr int kPanelStep = 256;           // columns of the widest tile, whole scale blocks
+
+int wgrad(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales, int M, int N, int K, void* dW, bool f32,
+          unsigned int* err, cudaStream_t st) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return RBQ_EINVAL;
+  const long long fits = kPanelBytes / (2ll * M) / kPanelStep * kPanelStep;
+  const int panel = static_cast<int>(std::min<long long>(K, std::max<long long>(fits, kPanelStep)));
+  for (int k0 = 0; k0 < K; k0 += panel) {
+    const int rc = wgrad_panel(dY, codes, scales, M, N, K, k0, std::min(panel, K - k0), dW, f32, err, dev, st);
+    if (rc != RBQ_OK) return rc;
+  }
+  return RBQ_OK;
 }
 
 }  // namespace

@@ -349,3 +349,42 @@ def test_native_and_python_calls_accept_the_same(monkeypatch):
         if r1 is not None:
             assert len(r1) == len(r2) and all(a.dtype == b.dtype and a.shape == b.shape for a, b in zip(r1, r2)), what
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(r1, r2) if a.numel()), what
+
+
+# ---- the weight gradient's workspace ----------------------------------------------------
+
+# Panels of 15104 and 1280 columns, the second in several parts; of 1024 and 528, both in parts.
+@pytest.mark.parametrize("M,N,K", [(70001, 16, 16384), (1000001, 40, 1552)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weight_gradient_in_panels(M, N, K, dtype):
+    """More than 2 GiB of BF16 values: panel by panel, exact as test_weight_gradient_counts_every_token."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    v = torch.randint(1, 4, (M, K), device="cuda", generator=g, dtype=torch.int8)
+    e = torch.randint(0, 3, (M, -(-K // 128)), device="cuda", generator=g, dtype=torch.uint8)
+    rows = torch.arange(M, device="cuda") % N
+    up = torch.randint(1, 4, (M,), device="cuda", generator=g)
+    dy = torch.zeros(M, N, device="cuda", dtype=torch.bfloat16)
+    dy[torch.arange(M, device="cuda"), rows] = up.bfloat16()
+    buf = torch.full((N + 2, K), 7.0, dtype=dtype, device="cuda")
+    rbq.qlinear_fp8_wgrad(dy, v.float().to(F8), (e + 127).view(E8), out=buf[1:-1])
+    assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+    for k in range(0, K, 128):
+        a = v[:, k:k + 128].double() * torch.exp2(e[:, k // 128:k // 128 + 1].double())
+        ref = torch.zeros(N, a.shape[1], device="cuda", dtype=torch.float64).index_add_(0, rows, a * up[:, None])
+        assert float(ref.max()) < 2 ** 24 and torch.equal(buf[1:-1, k:k + 128], ref.to(dtype)), k
+
+
+def test_weight_gradient_workspace_is_bounded():
+    """300000 x 16384 values would take 9.8 GB as BF16; the call takes 2 GiB of the device's free memory (it
+    stays in the library's pool) and what the driver adds."""
+    M, N, K = 300000, 64, 16384
+    q = torch.zeros(M, K, dtype=torch.uint8, device="cuda").view(F8)
+    s = torch.full((M, K // 128), 127, dtype=torch.uint8, device="cuda").view(E8)
+    dy = torch.ones(M, N, dtype=torch.bfloat16, device="cuda")
+    out = torch.ones(N, K, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    rbq.qlinear_fp8_wgrad(dy, q, s, out=out)
+    torch.cuda.synchronize()
+    assert before - torch.cuda.mem_get_info()[0] <= (2 << 30) + (256 << 20)
+    assert not out.any()
