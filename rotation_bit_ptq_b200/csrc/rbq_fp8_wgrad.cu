@@ -496,10 +496,11 @@ int wgrad_panel(const uint16_t* dY, const uint8_t* codes, const uint8_t* scales,
   uint16_t* x = static_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + x_bytes);
 
-  // rows per CTA: enough CTAs to fill the GPU, at most 65535 along y
+  // rows per CTA: while eight CTAs to an SM remain, at most 65535 along y
   const int xs = (cols + 4095) / 4096;
-  int rows = 1;
-  while (rows < 8 && static_cast<long long>(xs) * M / (2 * rows) >= 148 * 8) rows *= 2;
+  int rows = 1, sms = 148;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  while (rows < 8 && static_cast<long long>(xs) * M / (2 * rows) >= 8 * sms) rows *= 2;
   while ((M + rows - 1) / rows > 65535) rows *= 2;
   int rc = launch(decode_rows_kernel, dim3(xs, (M + rows - 1) / rows, 1), 256, 0, false, st, codes, scales, M, K,
                   blocks(K), cols, rows, x);
