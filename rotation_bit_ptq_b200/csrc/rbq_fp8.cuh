@@ -72,10 +72,9 @@ __device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
 }
 
 // True in one thread of a converged warp, the one that issues its MMAs or its
-// TMA copies.  The operands of both are uniform registers: under a test of the
-// lane number the compiler moves each of them there by a loop over the threads
-// that might be active (173 cycles a tcgen05.mma; a 256 x 256 x 32 one runs for
-// 128), under elect.sync it knows that there is one.
+// TMA copies.  Issued under a test of the lane number a tcgen05.mma took 173
+// cycles whatever its size; a 256 x 256 x 32 one runs for 128, and takes those
+// under elect.sync.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(

@@ -29,8 +29,9 @@
 // 2. fp8_few_kernel (few tokens): bound by reading the weights.  The weights
 //    take the MMA's M side (128 rows), the tokens its N side, and the CTAs of
 //    a cluster split K, each summing its part; the partial sums meet through
-//    distributed shared memory in a fixed order.  1 x 4096 x 4096 takes 4.9 us
-//    with the weights in L2 and 6.3 from HBM, 1 x 16384 x 4096 12.4 us (5.4 TB/s).
+//    distributed shared memory in a fixed order.  8 x 4096 x 4096 takes 4.9 us
+//    with the weights in L2 and 6.4 from HBM, 1 x 16384 x 4096 8.2 and 12.8 us
+//    (5.3 TB/s).
 // 3. fp8_dot_kernel (one to four tokens and not too many weights): CUDA cores.
 //
 // Every mbarrier wait is bounded; a thread whose wait runs out raises a shared
@@ -387,11 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) {
     // ---------------- MMA issuer (the even CTA's) ----------------
-    // The warp goes through the loop together and one thread issues, so that
-    // everything an MMA takes is uniform to the compiler.  With one thread in the whole loop it moved
-    // values from register to register for each MMA, more or fewer of them with every change to the kernel: 532 to
-    // 620 cycles a slice.  (fp8_few_kernel's loop is short, and the joint waits cost it more: 5.2 us in place of 4.9
-    // for 1 x 4096 x 4096.)
+    // The warp goes through the loop together and one thread issues.  With one
+    // thread in the whole loop a slice took 532 to 620 cycles, another number
+    // after every change to the kernel; 4096 x 16384 x 4096 went from 198 to 186 us
+    // together with the output by TMA.  (fp8_few_kernel's loop is short, and the
+    // joint waits cost it more: 5.2 us in place of 4.9 for 1 x 4096 x 4096.)
     if (rank == 0) {
       constexpr uint32_t kIdesc = idesc_mx(2 * kBM, kBN);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(ops));
@@ -848,9 +849,9 @@ int encode_out_map(CUtensorMap* map, uint16_t* base, int M, int N) {
 // by 16, two to an instruction; then come the two scales, and the sum over the
 // CTA in a fixed order.  No tensor maps, no tensor memory, no cluster: besides
 // the weights' way a token pays for a launch and one reduction.  1 x 4096 x
-// 4096 takes 4.2 us (5.3 from HBM) and fp8_few_kernel 4.9 (6.1); 1 x 1536 x
-// 1536 2.0 and 3.6; with more tokens or weights the tensor cores win (4 x
-// 4096 x 4096: 8.3 and 4.9).  Eight rows or several groups of threads to a
+// 4096 takes 4.3 us (5.8 from HBM) and fp8_few_kernel 5.0 (6.1); 1 x 1536 x
+// 1536 1.9 and 3.4; with more tokens or weights the tensor cores win (4 x
+// 4096 x 4096: 8.6 and 5.0).  Eight rows or several groups of threads to a
 // CTA, or 4096 codes at once, were slower: 4.6 to 6.9 us.
 constexpr int kDotThreads = 128, kDotRows = 4, kDotTokens = 4;
 constexpr int kDotSpan = 16 * kDotThreads;        // codes of a row that a CTA takes at a time
@@ -1067,22 +1068,25 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 }
 
 // Which kernel, with how many tokens to a tile and how many CTAs to a tile's
-// K: what takes least by a linear model, in ns, of the times of 42 layers of 1
-// to 32760 tokens, 64 to 16384 outputs and 256 to 16384 inputs with every
-// choice of both (its choice was the best or within 3 % of it in all but one
-// of them, where it lost 12 %): a launch `start`, each K slice of a wave of
-// CTAs `slice` or what 17 TB/s take from L2 for all of them, each further wave
-// 5000 (2400 by pairs), a cluster's joint sum 600 + 200 S + 8 NT.
+// K: what takes least by a linear model, in ns: a launch `start`, each K slice of
+// a wave of CTAs `slice` or what 17 TB/s take from L2 for all of them, each
+// further wave 5000 (2400 by pairs), a cluster's joint sum 600 + 200 S + 8 NT.
+// One to four tokens: fp8_dot_kernel where 1200 + 0.15 N + (250 + 260 M) for
+// each 2048 codes of a row + (45 + 80 M) for a million weights is less.
 // Few tokens to a tile fill the GPU and share little; the pair kernel shares
 // most and pays from about 60 tiles of 256 x 256.  For instance 512 x 4096 x
-// 4096: 15.2 us by pairs, 11.2 with NT = 128 (S = 1), 13.3 with NT = 256 and
-// S = 2; 1 x 4096 x 4096: 5.1 us with S = 4, 6.5 with S = 1; 4096 x 4096 x 4096:
-// 52.4 us by pairs, 65.9 with NT = 256; 333 x 1001 x 1552: 6.0 us with NT = 32,
-// 11.1 by pairs.
-// One to four tokens: fp8_dot_kernel where 1200 + 0.15 N + (250 + 260 M) for
-// each 2048 codes of a row + (45 + 80 M) for a million weights is less (30
-// layers of 64 to 16384 outputs and 256 to 16384 inputs: the better kernel
-// in all of them).
+// 4096: 14.4 us by pairs, 9.7 with NT = 128 (S = 1), 12.1 with NT = 256 and
+// S = 2; 1 x 4096 x 4096 without the dot kernel: 5.0 us with S = 4, 6.2 with S =
+// 1; 4096 x 4096 x 4096: 56 us by pairs, 67 with NT = 256; 333 x 1001 x 1552:
+// 5.8 us with NT = 32, 10.6 by pairs.
+// Measured on 70 layers of 1 to 4096 tokens and seven weights of 64 x 256 to
+// 16384 x 4096, every choice in each: its choice is the best or within 7 % of
+// it in 63 of them with the weights in L2, and in 63 with the weights from HBM,
+// whose bytes it does not count.  It loses most where it does not know that
+// clusters leave SMs idle, so that S = 4 takes a second wave (333 x 1536 x 8960:
+// 17.9 us, 11.1 with NT = 64 and S = 2), to the dot kernel's latency from HBM (1 x
+// 1536 x 8960: 8.7, 6.0 with NT = 16 and S = 8) and, at a few microseconds, by
+// leaving K whole (8 x 1001 x 1552: 4.9, 3.9 with S = 4).
 constexpr int kDotPlan = -1;
 struct Plan {
   int NT, S;                // tokens to a tile (0: the pair kernel, kDotPlan), CTAs to a cluster

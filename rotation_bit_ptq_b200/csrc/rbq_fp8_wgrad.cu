@@ -438,15 +438,20 @@ int launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool pair,
 }
 
 // The width of a tile and the parts the tokens are split into: what takes least
-// by a linear model, in ns, of the times of 15 gradients of 16 to 32760 tokens
-// and 64 x 128 to 16384 x 4096 weights (its choice was the best or within 7 %
-// of it): `start` a launch, `slice` each 64 tokens or what 17 TB/s take from L2
-// for all of them, `wave` each further wave of tiles, and for the joint sum
-// 2300, 110 a part and 0.3 per thousand fp32 values moved.  Narrow tiles are
-// twice as many, wide ones read dY half as often: 1560 x 1536 x 1536 takes 11.7
-// us with 128 (no parts), 15.9 with 256 and 17.3 with 256 in two parts; 4096 x
-// 16384 x 4096 332 us with 256, 366 with 128; 3001 x 64 x 128 9.6 us in 5
-// parts, 13.1 in one.
+// by a linear model, in ns: `start` a launch, `slice` each 64 tokens or what 17
+// TB/s take from L2 for all of them, `wave` each further wave of tiles, and for
+// the joint sum 2300, 110 a part and 0.3 per thousand fp32 values moved.  Narrow
+// tiles are twice as many, wide ones read dY half as often: 1560 x 1536 x 1536
+// takes 12.5 us with 128 (no parts), 15.3 with 256 and 16.8 with 256 in two
+// parts; 4096 x 16384 x 4096 320 us with 256, 376 with 128; 4096 x 64 x 128 10.2
+// us in 8 parts, 18.3 in one.
+// The constants were fitted before the output left by TMA and the parts were
+// summed in groups: the model's times are too long where the result's bytes
+// count (it says 43 us for 64 x 16384 x 4096, which takes 34), its choice holds.
+// Measured on 62 gradients of 16 to 32760 tokens and eight weights of 64 x 128
+// to 16384 x 4096, BF16 and fp32, every choice in each: the best or within 7 % of
+// it in 119 of 124.  It loses most at 8000 x 1000 x 1552 (53.7 us, 42.4 with 256
+// in two parts) and 512 x 64 x 128 in fp32 (10.4 us, 8.6 in 8 parts).
 struct WPlan {
   int BK, parts;
 };
