@@ -388,3 +388,108 @@ def test_weight_gradient_workspace_is_bounded():
     torch.cuda.synchronize()
     assert before - torch.cuda.mem_get_info()[0] <= (2 << 30) + (256 << 20)
     assert not out.any()
+
+
+def test_captured_gradients_in_panels():
+    """Two gradients of two panels each in one graph, replayed on new inputs."""
+    M, N, K = 70001, 16, 16384
+    g = torch.Generator(device="cuda").manual_seed(0)
+    dy = torch.randn(M, N, device="cuda", generator=g).bfloat16()
+    aq, asc, _ = _integers(g, M, 256, 1, -3, 3)
+    aq = aq.view(torch.uint8).repeat(1, K // 256).view(F8)
+    asc = asc.view(torch.uint8).repeat(1, K // 256).view(E8)
+    rbq.qlinear_fp8_wgrad(dy, aq, asc)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = rbq.qlinear_fp8_wgrad(dy, aq, asc), rbq.qlinear_fp8_wgrad(dy, aq, asc, dtype=torch.float32)
+    dy.copy_(torch.randn(M, N, device="cuda", generator=g).bfloat16())
+    for _ in range(2):
+        for o in out:
+            o.zero_()
+        gr.replay()
+        ref = rbq.qlinear_fp8_wgrad(dy, aq, asc, dtype=torch.float32)
+        assert torch.equal(out[1], ref) and torch.equal(out[0], ref.bfloat16())
+
+
+# ---- large sizes ----------------------------------------------------------------------------
+
+def test_more_than_2_31_weights_and_gradients():
+    """The last rows of matrices of 2.3e9 values, against calls on those rows alone."""
+    N, K = 140032, 16384
+    tail = 256                                             # whole blocks of 128 rows
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    w[-tail:] = torch.randn(tail, K, device="cuda").bfloat16()
+    big = rbq.quantize_weights_fp8(w, transposed=True)
+    small = rbq.quantize_weights_fp8(w[-tail:].contiguous(), transposed=True)
+    cut = (big[0][-tail:], big[1][-2:], big[2][:, -tail:], big[3][:, -2:])
+    for b, s in zip(cut, small):
+        assert torch.equal(b.contiguous().view(torch.uint8), s.view(torch.uint8))
+    assert not big[0][:-tail].view(torch.uint8).any() and not big[2][:, :-tail].view(torch.uint8).any()
+    del big, small, cut
+    xq, xs = rbq.quantize_fp8(w)
+    big = rbq.gelu_backward_fp8(w, xq, xs, quantize=True)
+    small = rbq.gelu_backward_fp8(w[-3:].contiguous(), xq[-3:].contiguous(), xs[-3:].contiguous(), quantize=True)
+    for b, s in zip(big, small):
+        assert torch.equal(b[-3:].view(torch.uint8), s.view(torch.uint8))
+    del big
+    # a gradient of 2.3e9 codes: all tokens but the last three have no weight
+    dy = torch.zeros(N, 8, dtype=torch.bfloat16, device="cuda")
+    dy[torch.arange(N - 3, N), torch.arange(3)] = 1.0
+    dW = rbq.qlinear_fp8_wgrad(dy, xq, xs, dtype=torch.float32)
+    held = xq[-3:].float() * xs[-3:].float().repeat_interleave(128, 1)
+    assert torch.equal(dW[:3], held) and not dW[3:].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000003, 16), (5, 1000003, 48), (300, 1000003, 16), (1000003, 3, 16),
+                                   (1000003, 40, 144)])
+def test_layers_of_very_long_sides(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    aq, asc, a = _integers(g, M, K, 1, -2, 2)
+    wq, wsc, w = _integers(g, N, K, 128, -2, 2)
+    y = rbq.qlinear_fp8(aq, asc, wq, wsc)
+    assert torch.equal(y, (a @ w.t()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 1000000, 16), (1000001, 8, 16), (3, 8, 1000000 // 16 * 16)])
+def test_gradients_of_very_long_sides(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    aq, asc, a = _integers(g, M, K, 1, 1, 3)
+    dy = torch.randint(0, 2, (M, N), device="cuda", generator=g)
+    dW = rbq.qlinear_fp8_wgrad(dy.bfloat16(), aq, asc, dtype=torch.float32)
+    assert torch.equal(dW, (dy.double().t() @ a).float())
+
+
+# ---- the differentiable layer under torch's modes ---------------------------------------------
+
+def test_linear_under_torchs_modes():
+    """no_grad, inference_mode, autocast, a checkpointed segment, saved tensors kept on
+    the CPU and a graph kept for a second backward pass change nothing."""
+    from torch.utils.checkpoint import checkpoint
+    g = torch.Generator(device="cuda").manual_seed(0)
+    X = torch.randn(3, 50, 256, device="cuda", generator=g).bfloat16().requires_grad_()
+    W = (torch.randn(272, 256, device="cuda", generator=g) * 0.1).requires_grad_()
+    dy = torch.randn(3, 50, 272, device="cuda", generator=g).bfloat16()
+
+    def layer(x, w):
+        return rbq.linear_fp8(x, w, activation="gelu")
+
+    y = layer(X, W)
+    ref = torch.autograd.grad(y, (X, W), dy, retain_graph=True)
+    again = torch.autograd.grad(y, (X, W), dy)
+    assert all(torch.equal(a, b) for a, b in zip(ref, again))
+    with torch.no_grad():
+        assert torch.equal(layer(X, W), y) and not layer(X, W).requires_grad
+    with torch.inference_mode():
+        assert torch.equal(layer(X, W), y)
+        assert torch.equal(rbq.qlinear_fp8(*rbq.quantize_fp8(X.flatten(0, 1), activation="gelu"),
+                                           *rbq.quantize_weights_fp8(W)).view(y.shape), y)
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        got = torch.autograd.grad(layer(X, W), (X, W), dy)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    got = torch.autograd.grad(checkpoint(layer, X, W, use_reentrant=False), (X, W), dy)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    with torch.autograd.graph.save_on_cpu():
+        y = layer(X, W)
+    got = torch.autograd.grad(y, (X, W), dy)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
