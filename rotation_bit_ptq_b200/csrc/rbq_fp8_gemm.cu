@@ -1081,12 +1081,12 @@ int launch_few(const uint8_t* a, const uint8_t* w, const Params& p, int S, int d
 // 5.8 us with NT = 32, 10.6 by pairs.
 // Measured on 70 layers of 1 to 4096 tokens and seven weights of 64 x 256 to
 // 16384 x 4096, every choice in each: its choice is the best or within 7 % of
-// it in 63 of them with the weights in L2, and in 63 with the weights from HBM,
-// whose bytes it does not count.  It loses most where it does not know that
-// clusters leave SMs idle, so that S = 4 takes a second wave (333 x 1536 x 8960:
-// 17.9 us, 11.1 with NT = 64 and S = 2), to the dot kernel's latency from HBM (1 x
-// 1536 x 8960: 8.7, 6.0 with NT = 16 and S = 8) and, at a few microseconds, by
-// leaving K whole (8 x 1001 x 1552: 4.9, 3.9 with S = 4).
+// it in 65 of them with the weights in L2, and in 65 with the weights from HBM,
+// whose bytes it does not count.  It loses most where clusters leave SMs idle,
+// which it does not count either: of S = 4, 33 run at once and 36 do not (333 x
+// 1408 x 8960 10.4 us, 333 x 1536 x 8960 17.9; the latter 11.1 with NT = 64 and
+// S = 2), and, at a few microseconds, by leaving K whole (8 x 1001 x 1552: 4.9,
+// 3.9 with S = 4).
 constexpr int kDotPlan = -1;
 struct Plan {
   int NT, S;                // tokens to a tile (0: the pair kernel, kDotPlan), CTAs to a cluster
