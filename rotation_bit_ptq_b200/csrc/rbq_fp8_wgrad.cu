@@ -450,8 +450,9 @@ int launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool pair,
 // count (it says 43 us for 64 x 16384 x 4096, which takes 34), its choice holds.
 // Measured on 62 gradients of 16 to 32760 tokens and eight weights of 64 x 128
 // to 16384 x 4096, BF16 and fp32, every choice in each: the best or within 7 % of
-// it in 118 of 124.  It loses most where narrow tiles fill one wave and a part
-// of another (8000 x 1000 x 1552: 52 us, 40 to 46 with 256 in two parts).
+// it in 118 of 124.  It loses most where the rows of dY and of x both begin off
+// 128-byte lines, which it does not count (8000 x 1000 x 1552: 50 us, 40 to 46 with
+// 256 in two parts; 8000 x 1024 x 1552 34, 8000 x 1000 x 1536 33).
 struct WPlan {
   int BK, parts;
 };
